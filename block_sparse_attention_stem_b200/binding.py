@@ -5,7 +5,8 @@ library.  PyTorch supplies device memory and the current stream.  If the
 shared library is missing, importing this module raises; there is no fallback.
 
 Entry points mirror the C names: ``stem_plan``, ``stem_score``,
-``stem_select``, ``stem_bsa_fwd``, ``stem_prefill``,
+``stem_select``, ``stem_bsa_fwd``, ``stem_prefill``, for the paged cache
+``stem_cache_extend``, ``stem_rope`` and ``stem_tree_attn``, and
 ``stem_read_device_status``, ``stem_status_string``.
 """
 
@@ -23,12 +24,14 @@ LIB_PATH = os.path.join(HERE, "libstem.so")
 STEM_OK = 0
 STATUS_NAMES = {0: "STEM_OK", 1: "STEM_ERR_INVALID_ARG", 2: "STEM_ERR_UNSUPPORTED",
                 3: "STEM_ERR_WORKSPACE_TOO_SMALL", 4: "STEM_ERR_MISALIGNED", 5: "STEM_ERR_CUDA",
-                6: "STEM_ERR_TIMEOUT", 7: "STEM_ERR_BAD_BLOCKLIST"}
+                6: "STEM_ERR_TIMEOUT", 7: "STEM_ERR_BAD_BLOCKLIST", 8: "STEM_ERR_BAD_INPUT",
+                9: "STEM_ERR_OUT_OF_PAGES"}
 STEM_BF16, STEM_FP8_E4M3 = 0, 1
 EXPORTED = ("stem_plan", "stem_score", "stem_select", "stem_score_select", "stem_bsa_fwd", "stem_bsa_fwd_paged",
             "stem_prefill",
             "stem_prefill_host",
             "stem_prefill_noalloc", "stem_noalloc_read_device_status",
+            "stem_cache_extend", "stem_rope", "stem_tree_plan", "stem_tree_attn",
             "stem_selftest_wait_timeout", "stem_read_device_status", "stem_status_string", "stem_version")
 
 
@@ -51,6 +54,38 @@ class StemQKV(ctypes.Structure):
 class StemPagedKV(ctypes.Structure):
     _fields_ = [("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
                 ("page_table", ctypes.c_void_p), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p)]
+
+
+class StemCacheStep(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32), ("num_free", ctypes.c_int32),
+                ("mask_words", ctypes.c_int32), ("cache_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+                ("held_pages", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("cursor", ctypes.c_void_p),
+                ("parents", ctypes.c_void_p)]
+
+
+class StemRope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_len", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class StemRopeIO(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("positions", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_scale", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p)]
+
+
+class StemTree(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("max_seq_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("mask_words", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("q_scale", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("softmax_scale", ctypes.c_double)]
 
 
 class StemPlan(ctypes.Structure):
@@ -84,6 +119,10 @@ def _load() -> ctypes.CDLL:
     lib.stem_prefill_noalloc.argtypes = [P(StemQKV), P(StemParams), vp, vp, vp, vp, vp]
     lib.stem_noalloc_read_device_status.argtypes = [vp, P(ctypes.c_int)]
     lib.stem_prefill_host.argtypes = [P(StemQKV), P(StemParams), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.stem_cache_extend.argtypes = [P(StemCacheStep)] + [vp] * 9 + [sz, vp]
+    lib.stem_rope.argtypes = [P(StemRope), P(StemRopeIO), P(StemPagedKV), vp]
+    lib.stem_tree_plan.argtypes = [P(StemTree), P(sz)]
+    lib.stem_tree_attn.argtypes = [P(StemTree), P(StemPagedKV), vp, vp, vp, sz, vp]
     lib.stem_selftest_wait_timeout.argtypes = [vp, vp]
     lib.stem_read_device_status.argtypes = [vp, vp, P(ctypes.c_int)]
     lib.stem_status_string.argtypes = [ctypes.c_int]
@@ -91,7 +130,7 @@ def _load() -> ctypes.CDLL:
     lib.stem_version.restype = ctypes.c_int32
     for name in ("stem_plan", "stem_score", "stem_select", "stem_bsa_fwd", "stem_prefill",
                  "stem_prefill_noalloc", "stem_noalloc_read_device_status", "stem_selftest_wait_timeout",
-                 "stem_read_device_status"):
+                 "stem_cache_extend", "stem_rope", "stem_tree_plan", "stem_tree_attn", "stem_read_device_status"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -354,6 +393,253 @@ def stem_noalloc_read_device_status(stream=None) -> int:
     _check(LIB.stem_noalloc_read_device_status(_stream(stream), ctypes.byref(out)),
            "stem_noalloc_read_device_status")
     return out.value
+
+
+# ------------------------------------------------------------------ the paged cache
+def _on(device, stream):
+    """The stream a call runs on: the caller's, or the current one of the tensors' device."""
+    if stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _need(name, t, dtype, shape=None, device=None):
+    """A contiguous tensor of the documented type, shape (None: any extent) and device."""
+    kinds = dtype if isinstance(dtype, tuple) else (dtype,)
+    if t.dtype not in kinds or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {' or '.join(str(k) for k in kinds)} tensor, got {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
+        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
+
+
+class _Device:
+    """Makes the tensors' device current for a call (a no-op when it is already)."""
+
+    def __init__(self, device):
+        self.index = device.index if device.type == "cuda" else None
+
+    def __enter__(self):
+        self.back = None
+        if self.index is not None and torch.cuda.current_device() != self.index:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+@dataclass
+class CacheStep:
+    """Outputs of stem_cache_extend (int32; the mask's words as int32 bit patterns)."""
+    held: torch.Tensor        # [S] pages held now
+    cursor: torch.Tensor      # [1] position in the free list
+    cu_seqlens: torch.Tensor  # [S + 1]
+    kv_lens: torch.Tensor     # [S]
+    slots: torch.Tensor       # [max_tokens]
+    positions: torch.Tensor   # [max_tokens]
+    mask: torch.Tensor | None  # [max_tokens, mask_words]
+    ws: torch.Tensor
+
+
+def stem_cache_extend(page_table, page_size: int, num_pages: int, cache_lens, new_lens, held_pages, free_pages, cursor,
+                      max_tokens: int, parents=None, mask_words: int = 0, out: CacheStep | None = None, ws=None,
+                      stream=None) -> CacheStep:
+    """Extends `page_table` [S, max_pages] in place by the pages that the step's
+    tokens need and returns the step's maps.  All tensors are int32 on the
+    device.  `out`: the buffers to write (its held, cursor and kv_lens may be
+    the input tensors, so that a captured step advances its own state).
+    Out-of-range values and an exhausted free list are reported in the
+    workspace's status word."""
+    dev = page_table.device
+    i32 = torch.int32
+    _need("page_table", page_table, i32, (None, None))
+    S = page_table.shape[0]
+    for name, t, shape in (("cache_lens", cache_lens, (S,)), ("new_lens", new_lens, (S,)),
+                           ("held_pages", held_pages, (S,)), ("free_pages", free_pages, (None,)),
+                           ("cursor", cursor, (1,))):
+        _need(name, t, i32, shape, dev)
+    tree = parents is not None
+    if tree:
+        _need("parents", parents, i32, (max_tokens,), dev)
+    words = mask_words if tree else 0
+    if out is None:
+        # one allocation; each part starts on a 16-byte boundary
+        sizes = (S, 1, S + 1, S, max_tokens, max_tokens, max_tokens * words)
+        buf = torch.empty(sum((n + 3) & ~3 for n in sizes), dtype=i32, device=dev)
+        parts, at = [], 0
+        for n in sizes:
+            parts.append(buf[at:at + n])
+            at += (n + 3) & ~3
+        out = CacheStep(*parts[:6], parts[6].view(max_tokens, words) if tree else None, None)
+    else:
+        for name, t, shape in (("held", out.held, (S,)), ("cursor", out.cursor, (1,)),
+                               ("cu_seqlens", out.cu_seqlens, (S + 1,)), ("kv_lens", out.kv_lens, (S,)),
+                               ("slots", out.slots, (max_tokens,)), ("positions", out.positions, (max_tokens,))):
+            _need("out." + name, t, i32, shape, dev)
+        if tree:
+            if out.mask is None:
+                raise ValueError("out.mask is needed with parents")
+            _need("out.mask", out.mask, i32, (max_tokens, words), dev)
+    out.ws = ws if ws is not None else out.ws if out.ws is not None else _ws(256, dev, None)
+    desc = StemCacheStep(S, max_tokens, page_size, num_pages, page_table.shape[1], free_pages.numel(), words,
+                         _ptr(cache_lens), _ptr(new_lens), _ptr(held_pages), _ptr(free_pages), _ptr(cursor),
+                         _ptr(parents))
+    with _Device(dev):
+        _check(LIB.stem_cache_extend(ctypes.byref(desc), _ptr(page_table), _ptr(out.held), _ptr(out.cursor),
+                                     _ptr(out.cu_seqlens), _ptr(out.kv_lens), _ptr(out.slots), _ptr(out.positions),
+                                     _ptr(out.mask) if tree else None, _ptr(out.ws), out.ws.numel(),
+                                     _on(dev, stream)), "stem_cache_extend")
+    return out
+
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def make_rope(rotary_dim=128, layout="half", base=1e6, scaling="plain", factor=1.0, original_len=1, beta_fast=32.0,
+              beta_slow=1.0, amplitude=0.0) -> StemRope:
+    """layout: a name of ROPE_LAYOUTS; scaling: one of ROPE_SCALINGS."""
+    return StemRope(ROPE_LAYOUTS[layout], rotary_dim, ROPE_SCALINGS[scaling], original_len, float(base), float(factor),
+                    float(beta_fast), float(beta_slow), float(amplitude))
+
+
+def _token_rows(name, t, T, device):
+    """Stride between the tokens of a bf16 [T, H, 128] tensor whose heads are contiguous."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T:
+        raise ValueError(f"{name} must be a bf16 [{T}, H, d] tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if T > 1 else t.shape[1] * t.shape[2]
+
+
+def stem_rope(rope: StemRope, q, k, v, positions, cache: PagedKV | None = None, slots=None, q_scale=None, k_scale=None,
+              v_scale=None, q_out=None, k_out=None, v_out=None, fp8: bool | None = None, stream=None):
+    """Rotates q [T, Hq, 128] and k [T, Hkv, 128] (bf16; slices of a fused
+    projection are fine) and stores k and v in the cache's pages at `slots`.
+    Returns (q_out, k_out, v_out): q_out is made when not given (unless q is
+    None), k_out and v_out are made only without a cache.  Outputs are bf16, or
+    e4m3 bytes (uint8) when the scales, fp32 [H], are given (or `fp8` says so).
+    v may be None without a cache; so may q or k."""
+    T = positions.numel()
+    dev = positions.device
+    _need("positions", positions, torch.int32, (T,))
+    if fp8 is None:
+        fp8 = q_scale is not None or k_scale is not None or v_scale is not None
+    kinds = (torch.uint8, torch.float8_e4m3fn) if fp8 else torch.bfloat16
+    heads = [0, 0, 0]
+    strides = [0, 0, 0]
+    for x, (name, t) in enumerate((("q", q), ("k", k), ("v", v))):
+        if t is not None:
+            strides[x], heads[x] = _token_rows(name, t, T, dev), t.shape[1]
+    if k is not None and v is not None and heads[1] != heads[2]:
+        raise ValueError("k and v must have the same heads")
+    hkv = heads[1] or heads[2]
+    d = next((t.shape[2] for t in (q, k, v) if t is not None), 128)
+    if cache is not None:
+        if slots is None or k is None or v is None:
+            raise ValueError("a cache needs k, v and slots")
+        _need("slots", slots, torch.int32, (T,), dev)
+        for name, p in (("k_pages", cache.k_pages), ("v_pages", cache.v_pages)):
+            _need(name, p, kinds, (None, None, hkv, d), dev)
+    make = lambda h: torch.empty(T, h, d, dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)  # noqa: E731
+    if q_out is None and q is not None:
+        q_out = make(heads[0])
+    if cache is None:
+        k_out = make(hkv) if k_out is None and k is not None else k_out
+        v_out = make(hkv) if v_out is None and v is not None else v_out
+    for name, t, h, sc in (("q", q_out, heads[0], q_scale), ("k", k_out, hkv, k_scale), ("v", v_out, hkv, v_scale)):
+        if t is not None:
+            _need(name + "_out", t, kinds, (T, h, d), dev)
+        if sc is not None:
+            _need(name + "_scale", sc, torch.float32, (h,), dev)
+    io = StemRopeIO(T, heads[0], hkv, d, STEM_FP8_E4M3 if fp8 else STEM_BF16, _ptr(positions), _ptr(slots), _ptr(q),
+                    _ptr(k), _ptr(v), *strides, _ptr(q_scale), _ptr(k_scale), _ptr(v_scale), _ptr(q_out), _ptr(k_out),
+                    _ptr(v_out))
+    with _Device(dev):
+        _check(LIB.stem_rope(ctypes.byref(rope), ctypes.byref(io), None if cache is None else ctypes.byref(cache.desc),
+                             _on(dev, stream)), "stem_rope")
+    return q_out, k_out, v_out
+
+
+@dataclass
+class TreeQ:
+    """The queries of one step and the descriptor that points at them; keeps
+    the tensors alive while the descriptor is used."""
+    q: torch.Tensor
+    cu_seqlens: torch.Tensor
+    kv_lens: torch.Tensor
+    mask: torch.Tensor | None
+    q_scale: torch.Tensor | None
+    k_scale: torch.Tensor | None
+    v_scale: torch.Tensor | None
+    desc: StemTree
+
+
+def make_tree(q, cu_seqlens, kv_lens, num_kv_heads: int, mask=None, max_seq_tokens: int = 0, q_scale=None, k_scale=None,
+              v_scale=None, softmax_scale: float = 0.0) -> TreeQ:
+    """q [T, Hq, 128] bf16, or e4m3 bytes with fp32 per-head scales; cu_seqlens
+    [S + 1], kv_lens [S] and mask [T, words] int32 on q's device.  Give
+    max_seq_tokens (the most queries of one sequence) where it is known: with 0
+    the launch is sized for T of them."""
+    dev = q.device
+    fp8 = q.dtype in (torch.uint8, torch.float8_e4m3fn)
+    _need("q", q, (torch.bfloat16, torch.uint8, torch.float8_e4m3fn), (None, None, None))
+    S = kv_lens.numel()
+    _need("kv_lens", kv_lens, torch.int32, (S,), dev)
+    _need("cu_seqlens", cu_seqlens, torch.int32, (S + 1,), dev)
+    if mask is not None:
+        _need("mask", mask, torch.int32, (q.shape[0], None), dev)
+    if fp8:
+        for name, t, h in (("q_scale", q_scale, q.shape[1]), ("k_scale", k_scale, num_kv_heads),
+                           ("v_scale", v_scale, num_kv_heads)):
+            if t is None:
+                raise ValueError(f"{name} is needed with e4m3 inputs")
+            _need(name, t, torch.float32, (h,), dev)
+    desc = StemTree(STEM_FP8_E4M3 if fp8 else STEM_BF16, S, q.shape[0], max_seq_tokens, q.shape[1], num_kv_heads,
+                    q.shape[2], 0 if mask is None else mask.shape[1], _ptr(cu_seqlens), _ptr(kv_lens), _ptr(mask),
+                    _ptr(q), _ptr(q_scale), _ptr(k_scale), _ptr(v_scale), float(softmax_scale))
+    return TreeQ(q, cu_seqlens, kv_lens, mask, q_scale, k_scale, v_scale, desc)
+
+
+def stem_tree_ws_bytes(tree: TreeQ) -> int:
+    out = ctypes.c_size_t(0)
+    _check(LIB.stem_tree_plan(ctypes.byref(tree.desc), ctypes.byref(out)), "stem_tree_plan")
+    return out.value
+
+
+def stem_tree_attn(tree: TreeQ, kv: PagedKV, out=None, lse=None, ws=None, stream=None):
+    """Attention of a step's queries over the paged cache: out bf16 [T, Hq, 128],
+    lse fp32 [Hq, T], and the workspace (whose status word tells of bad lengths)."""
+    q = tree.q
+    dev = q.device
+    T, hq, d = q.shape
+    fp8 = tree.desc.dtype == STEM_FP8_E4M3
+    kinds = (torch.uint8, torch.float8_e4m3fn) if fp8 else torch.bfloat16
+    for name, p in (("k_pages", kv.k_pages), ("v_pages", kv.v_pages)):
+        _need(name, p, kinds, (None, None, tree.desc.num_kv_heads, d), dev)
+    if kv.page_table.shape[0] < tree.desc.num_seqs or kv.page_table.device != dev:
+        raise ValueError("page_table must have a row per sequence, on the device of q")
+    if out is None:
+        out = torch.empty(T, hq, d, dtype=torch.bfloat16, device=dev)
+    else:
+        _need("out", out, torch.bfloat16, (T, hq, d), dev)
+    if lse is None:
+        lse = torch.empty(hq, T, dtype=torch.float32, device=dev)
+    else:
+        _need("lse", lse, torch.float32, (hq, T), dev)
+    if ws is None:
+        ws = _ws(stem_tree_ws_bytes(tree), dev, None)
+    with _Device(dev):
+        _check(LIB.stem_tree_attn(ctypes.byref(tree.desc), ctypes.byref(kv.desc), _ptr(out), _ptr(lse), _ptr(ws),
+                                  ws.numel(), _on(dev, stream)), "stem_tree_attn")
+    return out, lse, ws
 
 
 def stem_selftest_wait_timeout(ws, stream=None):

@@ -1,0 +1,905 @@
+// k_tree_attn.cu — attention of drafted trees, single tokens or causal chunks
+// over the paged cache.
+//
+//   O = sum_u exp2(c q.k_u - m) v_u / l,  m the running reference max, l the sum
+//
+// over the keys u of the sequence: all cached ones, and of the step's own
+// tokens those whose bit is set in the query's mask row.  The query heads of a
+// KV group and the tokens of a sequence share the keys, so they are the rows of
+// one 128-row tile (row = token * group + head), and the keys, 64 at a time
+// ("unit"), stream through tcgen05 as in the block-sparse kernel:
+//   S = Q K^T     tcgen05.mma M 128, N 64 into S buffer h % 2 (TMEM)
+//   P = exp2(..)  the softmax warps (thread = row = TMEM lane), over S
+//   O += P V      tcgen05.mma, P from TMEM, V from SMEM; O stays in TMEM
+//
+// Bound: every K/V byte once from HBM; a tile needs 4 * 128 FLOP per byte, so
+// the tensor cores are far from busy.  What matters is that all SMs stream all
+// the time, whatever the lengths: the units of all (sequence, KV head) items are
+// laid end to end and cut into equal ranges, one per CTA (two CTAs per SM).  A
+// range may hold the end of one item, several whole ones and the start of
+// another; whole ones are written at once, the at most two pieces go to the
+// workspace (fp32 O, m, l) and a second kernel joins them in range order.  The
+// cuts depend on the lengths alone, so results repeat bit for bit.  Sequences
+// with more than 128 rows have several tiles: the CTAs of one range (blockIdx =
+// range * tiles + tile) read the same keys at the same time, from L2.
+//
+// bf16: P is kept as a sum of two bf16 (15 significant bits; they fill the 64
+// columns of S exactly), so its rounding does not add to the output's: with a
+// single bf16 P the error of a long average is as large as the output rounding
+// itself.  The second product is free while HBM is the bound.  e4m3: Q K^T on
+// the e4m3 operands, P in f16, V widened to f16 (exact) by two warps per unit.
+//
+// Masked keys: S is replaced by -inf, so nothing in K matters.  A product 0 * v
+// would still carry a NaN or infinity of V into rows that do not see the key,
+// so in units that hold new tokens or the end of the sequence, rows of V behind
+// the end are zeroed in SMEM and non-finite elements of new tokens too; rows
+// that do see such an element get it added in the epilogue.
+//
+// 192 threads (256 for e4m3):
+//   warps 0-3  softmax, epilogue (TMEM lane quarter = warp)
+//   warp  4    TMA producer of Q, K and V
+//   warp  5    TMEM owner and MMA issuer    warps 6-7 (e4m3)  V -> f16
+// Every wait is bounded; on expiry all roles leave and the call reports it.
+#include "stem_bsa_common.cuh"
+
+namespace stem {
+
+namespace {
+
+constexpr int kUnit = 64;  // keys per S buffer
+constexpr int kProducer = 4, kMmaIssuer = 5, kWidenWarp = 6;
+constexpr uint32_t kTmemCols = 256;  // S buffers at 0 and 64, O at 128
+constexpr int kMinRange = 4;         // units below which a range is not cut further
+
+template <bool kFp8>
+struct TreeCfg {
+  static constexpr int kThreads = kFp8 ? 256 : 192;
+  static constexpr int kQBytes = kFp8 ? 16384 : 32768;
+  static constexpr int kSlabs = kFp8 ? 1 : 2;  // 128-byte slabs of a head row
+  static constexpr int kUnitBytes = kFp8 ? 8192 : 16384;
+  static constexpr int kKSlots = kFp8 ? 4 : 3;
+  static constexpr int kVSlots = kFp8 ? 4 : 2;
+};
+
+template <bool kFp8>
+struct TreeSmem {
+  using C = TreeCfg<kFp8>;
+  uint8_t q[C::kQBytes];  // 1024-aligned
+  uint8_t k[C::kKSlots][C::kUnitBytes];
+  uint8_t v[C::kVSlots][C::kUnitBytes];
+  uint8_t wide[kFp8 ? 2 : 1][kFp8 ? 16384 : 16];  // V as f16, e4m3 only
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[C::kKSlots], k_empty[C::kKSlots];
+  uint64_t v_full[C::kVSlots], v_empty[C::kVSlots];
+  uint64_t wide_full[2];
+  uint64_t s_full[2];   // S_h complete
+  uint64_t p_full[2];   // the softmax warps stored P_h (and rescaled O)
+  uint64_t pv_done[2];  // P_h V_h complete
+  uint64_t drain;
+  int64_t scan[16];
+  int64_t total, skip;  // units of the call; units of the first sequence before this range
+  int first_seq;
+  uint32_t tmem_base;
+  int status, abort;
+  int odd_v[4];  // [item % 4]: item + 1 when a non-finite element of V was zeroed in it
+};
+
+// Keys and queries of one sequence, as the call sees them.
+struct SeqShape {
+  int tok0, n, rows;  // first packed token, new tokens, tokens that are computed
+  int ctx, kv;        // keys before the new tokens (negative when some are not cached), end of the keys
+  int units;          // 0: nothing to do
+  bool bad;
+};
+
+__device__ __forceinline__ SeqShape seq_shape(const TreeArgs& a, int s) {
+  SeqShape r;
+  const int t0 = __ldg(a.cu_seqlens + s), t1 = __ldg(a.cu_seqlens + s + 1);
+  const int kv = max(__ldg(a.kv_lens + s), 0);
+  const int64_t cap = i64min(static_cast<int64_t>(a.max_pages) * a.page_size, 0x7fffff80);
+  r.bad = t0 < 0 || t1 < t0 || t1 > a.total_tokens;
+  r.tok0 = t0;
+  r.n = r.bad ? 0 : t1 - t0;
+  r.rows = min(r.n, a.max_seq_tokens);
+  r.ctx = kv - r.n;
+  r.kv = kv < cap ? kv : static_cast<int>(cap);
+  r.units = r.n == 0 ? 0 : max((r.kv + kUnit - 1) / kUnit, 1);
+  if (r.n > 0) r.bad |= r.rows < r.n || kv > cap || __ldg(a.kv_lens + s) < 0;
+  return r;
+}
+
+__device__ __forceinline__ int64_t range_begin(int64_t total, int ranges, int k) { return total * k / ranges; }
+// ranges in use: none is shorter than kMinRange units
+__device__ __forceinline__ int ranges_used(int64_t total, int most) {
+  return static_cast<int>(i64max(i64min(most, total / kMinRange), 1));
+}
+
+// Walks the items (sequence, KV head) of a range; every role walks alike.
+struct Walk {
+  int s, hk, unit;  // next item and its first unit
+  int64_t left;     // units of the range from there on
+  int index;        // items seen so far
+  SeqShape q;
+  // current item
+  int hk_cur, ub, ue;
+  bool whole;
+  __device__ __forceinline__ void start(const TreeArgs& a, int first_seq, int64_t skip, int64_t count) {
+    s = first_seq;
+    left = count;
+    index = 0;
+    q.units = 0;
+    if (count > 0) {
+      q = seq_shape(a, s);
+      hk = static_cast<int>(skip / q.units);
+      unit = static_cast<int>(skip % q.units);
+    }
+  }
+  // the next item whose sequence has this tile; false at the end of the range
+  __device__ __forceinline__ bool next(const TreeArgs& a, int tile) {
+    while (left > 0) {
+      if (hk == a.hkv) {
+        hk = 0;
+        do {
+          if (++s >= a.seqs) {  // the lengths changed under the call
+            left = 0;
+            return false;
+          }
+          q = seq_shape(a, s);
+        } while (q.units == 0);
+      }
+      hk_cur = hk;
+      ub = unit;
+      ue = static_cast<int>(i64min(q.units, unit + left));
+      whole = ub == 0 && ue == q.units;
+      left -= ue - ub;
+      unit = ue;
+      if (ue == q.units) {
+        unit = 0;
+        ++hk;
+      }
+      ++index;
+      if (tile * a.tile_tokens < q.rows) return true;
+    }
+    return false;
+  }
+};
+
+// Bits of the 64 keys from `key0` on that query i of the sequence sees.
+__device__ __forceinline__ uint64_t visible(const TreeArgs& a, const SeqShape& q, int i, int key0) {
+  const int d0 = key0 - q.ctx;  // index, among the new tokens, of the first key
+  uint64_t bits;
+  if (a.mask == nullptr) {
+    const int seen = i + 1 - d0;  // new tokens up to i, from the first key on
+    bits = seen <= 0 ? 0ull : seen >= 64 ? ~0ull : (1ull << seen) - 1;
+  } else {
+    const uint32_t* row = a.mask + static_cast<size_t>(q.tok0 + i) * a.mask_words;
+    const int from = max(d0, 0);
+    const int w = from >> 5, sh = from & 31;
+    auto word = [&](int x) -> uint64_t { return x < a.mask_words ? __ldg(row + x) : 0u; };
+    const uint64_t lo = word(w) | word(w + 1) << 32;
+    bits = sh == 0 ? lo : lo >> sh | word(w + 2) << (64 - sh);
+    if (q.n - from < 64) bits &= (1ull << (q.n - from > 0 ? q.n - from : 0)) - 1;
+    if (d0 < 0) bits = (d0 > -64 ? bits << -d0 | ((1ull << -d0) - 1) : ~0ull);
+  }
+  const int keys = q.kv - key0;
+  if (keys < 64) bits &= keys <= 0 ? 0ull : (1ull << keys) - 1;
+  return bits;
+}
+
+// Pool row of key u of sequence s, or the first row past the pool (reads zeros).
+__device__ __forceinline__ int pool_row(const TreeArgs& a, int s, int u) {
+  const int pg = u / a.page_size;
+  const int page = pg < a.max_pages ? __ldg(a.page_table + static_cast<size_t>(s) * a.max_pages + pg) : -1;
+  if (page < 0 || page >= a.num_pages) return a.num_pages * a.page_size;
+  return page * a.page_size + (u - pg * a.page_size);
+}
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Non-finite 16-bit elements (bf16: exponent 0xff) of a pair are zeroed.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& odd) {
+  if ((w & 0x7f80u) == 0x7f80u) {
+    w &= 0xffff0000u;
+    odd = true;
+  }
+  if ((w & 0x7f800000u) == 0x7f800000u) {
+    w &= 0x0000ffffu;
+    odd = true;
+  }
+  return w;
+}
+
+}  // namespace
+
+template <bool kFp8>
+__global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
+    tree_attn_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeArgs a) {
+  using Cfg = TreeCfg<kFp8>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  TreeSmem<kFp8>& sm = *reinterpret_cast<TreeSmem<kFp8>*>(smem_raw);
+  const int warp = warp_id(), lane = lane_id();
+  const int range = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- where this range starts: prefix sum of the sequences' units
+  if (threadIdx.x == 0) {
+    sm.status = 0;
+    sm.abort = (smem_u32(smem_raw) & 1023u) != 0;  // the swizzled tiles need this alignment
+    if (sm.abort) sm.status = STEM_ERR_TIMEOUT_CODE;
+    for (int x = 0; x < 4; ++x) sm.odd_v[x] = 0;
+  }
+  const int per = (a.seqs + Cfg::kThreads - 1) / Cfg::kThreads;
+  const int s_beg = min(static_cast<int>(threadIdx.x) * per, a.seqs), s_end = min(s_beg + per, a.seqs);
+  int64_t mine = 0;
+  bool bad = false;
+  for (int s = s_beg; s < s_end; ++s) {
+    const SeqShape q = seq_shape(a, s);
+    mine += q.units;
+    bad |= q.bad;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) sm.scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < Cfg::kThreads / 32; ++w) {
+    if (w < warp) before += sm.scan[w];
+    total += sm.scan[w];
+  }
+  before *= a.hkv;
+  mine *= a.hkv;
+  total *= a.hkv;
+  const int used = ranges_used(total, a.ranges);
+  const int64_t u0 = range < used ? range_begin(total, used, range) : total;
+  const int64_t count = range < used ? range_begin(total, used, range + 1) - u0 : 0;
+  if (bad && blockIdx.x == 0) set_status(&sm.status, STEM_ERR_BAD_INPUT_CODE);
+  if (blockIdx.x == 0) {
+    int64_t at = before;
+    for (int s = s_beg; s < s_end; ++s) {
+      a.unit0[s] = at;
+      at += static_cast<int64_t>(seq_shape(a, s).units) * a.hkv;
+    }
+    if (threadIdx.x == 0) a.unit0[a.seqs] = total;
+  }
+  if (count > 0 && before <= u0 && u0 < before + mine) {
+    int64_t at = before;
+    int s = s_beg;
+    for (;; ++s) {
+      const int64_t more = static_cast<int64_t>(seq_shape(a, s).units) * a.hkv;
+      if (u0 < at + more) break;
+      at += more;
+    }
+    sm.first_seq = s;
+    sm.skip = u0 - at;
+  }
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.q_full[b], 1);
+      mbar_init(&sm.q_empty[b], 1);
+      mbar_init(&sm.wide_full[b], 2);
+      mbar_init(&sm.s_full[b], 1);
+      mbar_init(&sm.p_full[b], 4);
+      mbar_init(&sm.pv_done[b], 1);
+    }
+    for (int b = 0; b < Cfg::kKSlots; ++b) {
+      mbar_init(&sm.k_full[b], 1);
+      mbar_init(&sm.k_empty[b], 1);
+    }
+    for (int b = 0; b < Cfg::kVSlots; ++b) {
+      mbar_init(&sm.v_full[b], 1);
+      mbar_init(&sm.v_empty[b], kFp8 ? 2 : 1);
+    }
+    mbar_init(&sm.drain, 1);
+    fence_mbar_init();
+  }
+  if (count == 0) {
+    __syncthreads();
+    if (threadIdx.x == 0) a.cta_status[blockIdx.x] = sm.status;
+    return;
+  }
+  if (warp == kMmaIssuer) {
+    tmem_alloc(&sm.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  int* status = &sm.status;
+  Walk wk;
+  wk.start(a, sm.first_seq, sm.skip, count);
+  // Q tiles of at most 64 rows have two buffers, so that the next item's
+  // products need not wait for the last one's
+  const int qbufs = a.box_rows <= 64 ? 2 : 1;
+  const int qslab = 16384 / qbufs;  // bytes of a slab
+
+  if (warp == kProducer) {
+    // ------------------------------------------------------------ producer
+    // Lane 0 issues; the warp looks up 32 units' pages at a time.  K runs ahead
+    // of V by `ahead` units.  While V_h is the next V, the products up to
+    // S_{h+1} can complete, and the Q tile of K_{h+ahead-1} may have to wait for
+    // S_{h+ahead-1-qbufs} (items of one unit): hence ahead <= 2 + qbufs.
+    if (lane == 0) {
+      tma_prefetch_desc(&maps.q);
+      tma_prefetch_desc(&maps.k_pool);
+      tma_prefetch_desc(&maps.v_pool);
+    }
+    struct Stream {
+      Walk w;
+      int u, rows, h, slot, round;
+      bool more;
+    };
+    Stream ks{wk, 0, 0, 0, 0, 0, false}, vs{wk, 0, 0, 0, 0, 0, false};
+    int item = 0;  // Q tiles issued
+    bool ok = !*abort;
+    auto enter = [&](Stream& st) {
+      st.more = st.w.next(a, tile);
+      if (st.more) st.u = st.w.ub;
+    };
+    // issues the stream's next unit; false when a wait ran out
+    auto load = [&](Stream& st, const CUtensorMap* m, uint8_t* base, uint64_t* full, uint64_t* empty, int slots) -> bool {
+      const int x = (st.u - st.w.ub) & 31;
+      if (x == 0) st.rows = pool_row(a, st.w.s, min(st.u + lane, st.w.ue - 1) * kUnit);
+      const int row = __shfl_sync(0xffffffffu, st.rows, x);
+      bool good = true;
+      if (lane == 0) {
+        if (st.round > 0) good = mbar_wait(&empty[st.slot], (st.round - 1) & 1, abort, status);
+        if (good) {
+          mbar_arrive_expect_tx(&full[st.slot], Cfg::kUnitBytes);
+          for (int y = 0; y < Cfg::kSlabs; ++y)
+            tma_load_3d(base + st.slot * Cfg::kUnitBytes + y * (kUnit * 128), m, &full[st.slot], y * 64, st.w.hk_cur, row);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, good, 0)) return false;
+      ++st.h;
+      if (++st.slot == slots) {
+        st.slot = 0;
+        ++st.round;
+      }
+      ++st.u;
+      return true;
+    };
+    auto load_k = [&]() -> bool {
+      if (ks.u == ks.w.ub) {
+        bool good = true;
+        if (lane == 0) {
+          const int b = item % qbufs;
+          if (item >= qbufs) good = mbar_wait(&sm.q_empty[b], (item / qbufs - 1) & 1, abort, status);
+          if (good) {
+            mbar_arrive_expect_tx(&sm.q_full[b], a.box_rows * 128 * Cfg::kSlabs);
+            for (int x = 0; x < Cfg::kSlabs; ++x)
+              tma_load_3d(sm.q + (b * Cfg::kSlabs + x) * qslab, &maps.q, &sm.q_full[b], x * 64, ks.w.hk_cur * a.group,
+                          ks.w.q.tok0 + tile * a.tile_tokens);
+          }
+        }
+        if (!__shfl_sync(0xffffffffu, good, 0)) return false;
+        ++item;
+      }
+      if (!load(ks, &maps.k_pool, sm.k[0], sm.k_full, sm.k_empty, Cfg::kKSlots)) return false;
+      if (ks.u == ks.w.ue) enter(ks);
+      return true;
+    };
+    if (ok) {
+      enter(ks);
+      enter(vs);
+    }
+    const int ahead = min(Cfg::kKSlots, 2 + qbufs);
+    for (int x = 0; x < ahead && ok && ks.more; ++x) ok = load_k();
+    while (ok && vs.more) {
+      ok = load(vs, &maps.v_pool, sm.v[0], sm.v_full, sm.v_empty, Cfg::kVSlots);
+      if (ok && vs.u == vs.w.ue) enter(vs);
+      if (ok && ks.more) ok = load_k();
+    }
+    // every copy has landed before the CTA can exit (a slot or Q buffer has at
+    // most one copy in flight)
+    if (lane == 0) {
+      auto quiesce = [&](uint64_t* full, int slots, int n) {
+        for (int x = 0; x < slots && x < n; ++x) {
+          const int last = n - 1 - (n - 1 - x) % slots;
+          mbar_wait_quiesce(&full[x], (last / slots) & 1, status);
+        }
+      };
+      quiesce(sm.k_full, Cfg::kKSlots, ks.h);
+      quiesce(sm.v_full, Cfg::kVSlots, vs.h);
+      quiesce(sm.q_full, qbufs, item);
+    }
+    __syncwarp();
+  } else if (warp == kMmaIssuer) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_s = make_idesc(kFp8 ? 0u : 1u, 0u, 128u, static_cast<uint32_t>(kUnit));
+      const uint32_t idesc_o = make_idesc(kFp8 ? 0u : 1u, 1u, 128u, 128u);
+      const uint32_t o_tmem = tmem + 128;
+      // two walks: S runs two units ahead of P V
+      Walk ws = wk;
+      int hs = 0, us = 0, qitem = -1;
+      bool more_s = ws.next(a, tile);
+      if (more_s) us = ws.ub;
+      auto issue_s = [&]() -> bool {
+        if (us == ws.ub) {
+          ++qitem;
+          if (!mbar_wait(&sm.q_full[qitem % qbufs], (qitem / qbufs) & 1, abort, status)) return false;
+        }
+        const int slot = hs % Cfg::kKSlots;
+        if (!mbar_wait(&sm.k_full[slot], (hs / Cfg::kKSlots) & 1, abort, status)) return false;
+        tc_fence_after();
+        const uint32_t sq = smem_u32(sm.q) + (qitem % qbufs) * Cfg::kSlabs * qslab;
+        const uint32_t sk = smem_u32(sm.k[slot]);
+        const uint32_t d = tmem + kUnit * (hs & 1);
+        if constexpr (kFp8) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f8_ss(d, make_sdesc_sw128(sq + kk * 32, 16, 1024), make_sdesc_sw128(sk + kk * 32, 16, 1024), idesc_s,
+                      kk != 0);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ss(d, make_sdesc_sw128(sq + (kk >> 2) * qslab + (kk & 3) * 32, 16, 1024),
+                        make_sdesc_sw128(sk + (kk >> 2) * (kUnit * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk != 0);
+        }
+        mma_commit(&sm.k_empty[slot]);
+        mma_commit(&sm.s_full[hs & 1]);
+        ++hs;
+        if (++us == ws.ue) {
+          mma_commit(&sm.q_empty[qitem % qbufs]);
+          more_s = ws.next(a, tile);
+          if (more_s) us = ws.ub;
+        }
+        return true;
+      };
+      bool ok = !*abort;
+      for (int x = 0; x < 2 && ok && more_s; ++x) ok = issue_s();
+      int h = 0;
+      while (ok && wk.next(a, tile)) {
+        for (int u = wk.ub; u < wk.ue && ok; ++u, ++h) {
+          const int slot = h % Cfg::kVSlots;
+          uint64_t* vbar = kFp8 ? &sm.wide_full[h & 1] : &sm.v_full[slot];
+          ok = mbar_wait(&sm.p_full[h & 1], (h >> 1) & 1, abort, status) &&
+               mbar_wait(vbar, (kFp8 ? h >> 1 : h / Cfg::kVSlots) & 1, abort, status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sv = smem_u32(kFp8 ? sm.wide[h & 1] : sm.v[slot]);
+          const uint32_t p = tmem + kUnit * (h & 1);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 16 keys per step
+            mma_bf16_ts(o_tmem, p + kk * 8, make_sdesc_sw128(sv + kk * 2048, kUnit * 128, 1024), idesc_o,
+                        u != wk.ub || kk != 0);
+          if constexpr (!kFp8) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // the low parts of P
+              mma_bf16_ts(o_tmem, p + 32 + kk * 8, make_sdesc_sw128(sv + kk * 2048, kUnit * 128, 1024), idesc_o, 1u);
+            mma_commit(&sm.v_empty[slot]);
+          }
+          mma_commit(&sm.pv_done[h & 1]);
+          if (more_s) ok = issue_s();
+        }
+      }
+      mma_commit(&sm.drain);
+      mbar_wait_quiesce(&sm.drain, 0, status);
+    }
+    __syncwarp();
+  } else if (kFp8 && warp >= kWidenWarp) {
+    // ------------------------------------------------------------ V -> f16
+    if constexpr (kFp8) {
+      const int t = (warp - kWidenWarp) * 32 + lane;
+      const int c = t & 7;  // 16-byte chunk of the e4m3 row
+      int h = 0;
+      bool ok = !*abort;
+      for (int item = 0; ok && wk.next(a, tile); ++item) {
+        for (int u = wk.ub; u < wk.ue; ++u, ++h) {
+          const int slot = h % Cfg::kVSlots;
+          ok = mbar_wait(&sm.v_full[slot], (h / Cfg::kVSlots) & 1, abort, status) &&
+               (h < 2 || mbar_wait(&sm.pv_done[h & 1], ((h - 2) >> 1) & 1, abort, status));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* src = sm.v[slot];
+          uint8_t* dst = sm.wide[h & 1] + (c >> 2) * (kUnit * 128);
+          const bool check = (u + 1) * kUnit > wk.q.ctx;
+          const int end = wk.q.kv - u * kUnit;  // rows from here on are behind the keys
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = (t >> 3) + 8 * i;
+            uint4 x = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
+            uint32_t w[8];
+            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              w[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[e] & 0xffffu));
+              w[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[e] >> 16));
+            }
+            if (check) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if (r >= end) w[e] = 0u;
+                if ((w[e] & 0x7c00u) == 0x7c00u) {
+                  w[e] &= 0xffff0000u;
+                  odd = true;
+                }
+                if ((w[e] & 0x7c000000u) == 0x7c000000u) {
+                  w[e] &= 0x0000ffffu;
+                  odd = true;
+                }
+              }
+            }
+            // elements 16 c .. 16 c + 15: chunks 2 (c % 4) and + 1 of slab c / 4;
+            // the two slabs' lanes write opposite halves first (other banks)
+            const int o = 2 * (c & 3), f = c >> 2;
+            uint8_t* row = dst + r * 128;
+            *reinterpret_cast<uint4*>(row + (((o + f) ^ (r & 7)) << 4)) =
+                f ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(row + (((o + 1 - f) ^ (r & 7)) << 4)) =
+                f ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          if (odd) sm.odd_v[item & 3] = item + 1;  // at most two items ahead of the epilogue
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.wide_full[h & 1]);
+            mbar_arrive(&sm.v_empty[slot]);
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax + epilogue
+    const int row = warp * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t o_tmem = tmem + 128 + lane_off;
+    const float ninf = -__int_as_float(0x7f800000);
+    const int g = row % a.group, ti = row / a.group;  // head of the group, token of the tile
+    int h = 0;
+    bool ok = !*abort;
+    for (int item = 0; ok && wk.next(a, tile); ++item) {
+      const int i = tile * a.tile_tokens + ti;  // token of the sequence
+      const bool valid = ti < a.tile_tokens && i < wk.q.rows;
+      const bool active = __any_sync(0xffffffffu, valid);
+      const int hq = wk.hk_cur * a.group + g;
+      float c = a.scale_log2;
+      if constexpr (kFp8) c *= __ldg(a.q_scale + hq) * __ldg(a.k_scale + wk.hk_cur);
+      float m_ref = ninf, l = 0.f;
+#pragma unroll 1
+      for (int u = wk.ub; u < wk.ue; ++u, ++h) {
+        const int b = h & 1;
+        const uint32_t s_tmem = tmem + kUnit * b + lane_off;
+        const bool edge = (u + 1) * kUnit > wk.q.ctx;  // new tokens or the end of the keys
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.s_full[b], (h >> 1) & 1, abort, status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (!kFp8 && edge) {
+          // no NaN or infinity of V may meet a weight of zero
+          const int slot = h % Cfg::kVSlots;
+          if (!__all_sync(0xffffffffu, mbar_wait(&sm.v_full[slot], (h / Cfg::kVSlots) & 1, abort, status))) {
+            ok = false;
+            break;
+          }
+          const int end = wk.q.kv - u * kUnit;
+          bool odd = false;
+#pragma unroll 1
+          for (int x = row; x < 2 * kUnit * 8; x += 128) {
+            const int r = (x >> 3) & (kUnit - 1);  // 16-byte chunk x of the two slabs: row r
+            const int key = u * kUnit + r;
+            if (key < wk.q.ctx) continue;
+            uint4* at = reinterpret_cast<uint4*>(sm.v[slot] + x * 16);
+            uint4 w = *at;
+            if (r >= end) w = make_uint4(0u, 0u, 0u, 0u);
+            w.x = finite_bf16x2(w.x, odd);
+            w.y = finite_bf16x2(w.y, odd);
+            w.z = finite_bf16x2(w.z, odd);
+            w.w = finite_bf16x2(w.w, odd);
+            *at = w;
+          }
+          if (odd) sm.odd_v[item & 3] = item + 1;
+          fence_async_smem();
+        }
+        if (active) {
+          uint32_t rr[2][32];
+          tmem_ld32(s_tmem, rr[0]);
+          tmem_ld32(s_tmem + 32, rr[1]);
+          tmem_ld_wait();
+          if (edge) {
+            const uint64_t see = valid ? visible(a, wk.q, i, u * kUnit) : 0ull;
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              const uint32_t bits = static_cast<uint32_t>(see >> (32 * ch));
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (!((bits >> x) & 1u)) rr[ch][x] = 0xff800000u;  // -inf
+            }
+          }
+          float m4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m4[e] = fmax3(__uint_as_float(rr[e >> 1][(e & 1) * 16]), __uint_as_float(rr[e >> 1][(e & 1) * 16 + 1]),
+                          __uint_as_float(rr[e >> 1][(e & 1) * 16 + 2]));
+#pragma unroll
+          for (int x = 3; x < 15; x += 2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              m4[e] = fmax3(m4[e], __uint_as_float(rr[e >> 1][(e & 1) * 16 + x]),
+                            __uint_as_float(rr[e >> 1][(e & 1) * 16 + x + 1]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(rr[e >> 1][(e & 1) * 16 + 15]));
+          const float m_cand = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c;
+          const bool need =
+              valid && ((m_ref == ninf) ? (m_cand != ninf) : (m_cand > m_ref + BsaCfg<kFp8>::kRescaleLog2));
+          if (__any_sync(0xffffffffu, need)) {
+            const float m_new = need ? m_cand : m_ref;
+            const float alpha = (m_ref == ninf) ? 0.f : fast_exp2(m_ref - m_new);
+            l *= alpha;
+            if (u > wk.ub) {
+              // O holds P V up to the unit before: let that product finish first
+              if (!__all_sync(0xffffffffu,
+                              mbar_wait(&sm.pv_done[b ^ 1], ((h - 1) >> 1) & 1, abort, status))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll 1
+              for (int ch = 0; ch < 4; ++ch) {
+                uint32_t oo[32];
+                tmem_ld32(o_tmem + ch * 32, oo);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) oo[x] = __float_as_uint(__uint_as_float(oo[x]) * alpha);
+                tmem_st32(o_tmem + ch * 32, oo);
+              }
+            }
+            m_ref = m_new;
+          }
+          const float m_use = (m_ref == ninf) ? 0.f : m_ref;
+          const float2 c2 = make_float2(c, c), nm2 = make_float2(-m_use, -m_use);
+          float2 ps0 = make_float2(0.f, 0.f), ps1 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float2 e = ffma2(
+                  make_float2(__uint_as_float(rr[ch][2 * x]), __uint_as_float(rr[ch][2 * x + 1])), c2, nm2);
+              const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+              if (x & 1) ps1 = fadd2(ps1, p);
+              else ps0 = fadd2(ps0, p);
+              if constexpr (kFp8) {
+                hi[x] = f32x2_to_f16x2(p.x, p.y);
+              } else {
+                // hi: the largest bf16 below p (p (1 - 2^-24) rounds to the float before p),
+                // so that both parts of a weight above zero are above zero and an
+                // infinity of V stays one
+                const float2 e = fmul2(p, make_float2(0.99999994f, 0.99999994f));
+                const uint32_t e0 = __float_as_uint(e.x) & 0xffff0000u, e1 = __float_as_uint(e.y) & 0xffff0000u;
+                hi[x] = __byte_perm(e0, e1, 0x7632);
+                const float2 r = fsub2(p, make_float2(__uint_as_float(e0), __uint_as_float(e1)));
+                lo[x] = pack_bf16x2(r.x, r.y);
+              }
+            }
+            tmem_st16(s_tmem + 16 * ch, hi);
+            if constexpr (!kFp8) tmem_st16(s_tmem + 32 + 16 * ch, lo);
+          }
+          l += (ps0.x + ps0.y) + (ps1.x + ps1.y);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[b]);
+      }
+      if (!ok) break;
+
+      // ---- epilogue of the item: h - 1 is its last unit
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.pv_done[(h - 1) & 1], ((h - 1) >> 1) & 1, abort, status))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // every sanitised V of the item is behind a wait of this thread, so the flag is seen
+      const bool odd_v = *reinterpret_cast<volatile int*>(&sm.odd_v[item & 3]) == item + 1;
+      if (active) {
+        const size_t tok = static_cast<size_t>(wk.q.tok0) + i;
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (wk.index > 1 ? 1 : 0)) * a.part_rows + row;
+        float inv = (l != 0.f) ? 1.f / l : 0.f;
+        if constexpr (kFp8) inv *= __ldg(a.v_scale + wk.hk_cur);
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t rr[32];
+          tmem_ld32(o_tmem + ch * 32, rr);
+          tmem_ld_wait();
+          if (odd_v && valid) {
+            // add the non-finite elements of V that this row does see
+            for (int u = max(wk.ub, wk.q.ctx / kUnit); u < wk.ue; ++u) {
+              uint64_t see = visible(a, wk.q, i, u * kUnit);
+              for (; see != 0ull; see &= see - 1) {
+                const int key = u * kUnit + __ffsll(static_cast<long long>(see)) - 1;
+                if (key < wk.q.ctx) continue;
+                const int pr = pool_row(a, wk.s, key);
+                if (pr >= a.num_pages * a.page_size) continue;
+                const uint8_t* v = a.v_pages + ((static_cast<size_t>(pr) * a.hkv + wk.hk_cur) * kHeadDim + ch * 32) *
+                                                   (kFp8 ? 1 : 2);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                  float e;
+                  if constexpr (kFp8) e = (v[x] & 0x7f) == 0x7f ? __int_as_float(0x7fffffff) : 0.f;
+                  else e = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(v)[x]) << 16);
+                  if ((__float_as_uint(e) & 0x7f800000u) == 0x7f800000u)
+                    rr[x] = __float_as_uint(__uint_as_float(rr[x]) + e);
+                }
+              }
+            }
+          }
+          if (!valid) continue;
+          if (wk.whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) +
+                                                  (tok * a.hq + hq) * static_cast<size_t>(kHeadDim) * 2) + ch * 4;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16x2(__uint_as_float(rr[q * 8 + 2 * e]) * inv,
+                                   __uint_as_float(rr[q * 8 + 2 * e + 1]) * inv);
+              dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * kHeadDim + ch * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[q] = make_uint4(rr[4 * q], rr[4 * q + 1], rr[4 * q + 2], rr[4 * q + 3]);
+          }
+        }
+        if (valid) {
+          if (wk.whole)
+            a.lse[static_cast<size_t>(hq) * a.total_tokens + tok] =
+                (l != 0.f) ? (m_ref + log2f(l)) * 0.69314718055994530942f : ninf;
+          else
+            a.part_ml[part] = make_float2(m_ref, l);
+        }
+      }
+      // the next item's first product into O waits for this warp's next P,
+      // which comes after these reads
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) a.cta_status[blockIdx.x] = sm.status;
+  if (warp == kMmaIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the pieces of the items that were cut: one block per (row, sequence x
+// KV head), its four warps take every fourth piece.  Block 0 also reduces the
+// CTAs' status.
+__global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas, int rows_per_block) {
+  __shared__ float sm_o[4][kHeadDim];
+  __shared__ float2 sm_ml[4];
+  __shared__ int sm_status;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = warp_id(), lane = lane_id();
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (threadIdx.x == 0) sm_status = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < ctas; i += 128) {
+      const int st = a.cta_status[i];
+      if (st != 0) atomicCAS(&sm_status, 0, st);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) *a.status = sm_status;
+  }
+  const float ninf = -__int_as_float(0x7f800000);
+  for (int item = blockIdx.y; item < a.seqs * a.hkv; item += gridDim.y) {
+    const int s = item / a.hkv, hk = item % a.hkv;
+    const int64_t at = a.unit0[s];
+    const int64_t units = (a.unit0[s + 1] - at) / a.hkv;
+    if (units == 0) continue;
+    const int64_t total = a.unit0[a.seqs];
+    const int used = ranges_used(total, a.ranges);
+    const int64_t first = at + hk * units, last = first + units - 1;
+    // the range that holds unit x: the largest k with range_begin(k) <= x
+    const int k0 = static_cast<int>(((first + 1) * used - 1) / total);
+    const int k1 = static_cast<int>(((last + 1) * used - 1) / total);
+    if (k0 == k1) continue;  // not cut
+    const SeqShape q = seq_shape(a, s);
+    const int slot0 = range_begin(total, used, k0) == first ? 0 : 1;
+    for (int r = blockIdx.x * rows_per_block; r < min((static_cast<int>(blockIdx.x) + 1) * rows_per_block, q.rows * a.group);
+         ++r) {
+      const int i = r / a.group, tile = i / a.tile_tokens;
+      const int row = r - tile * a.tile_tokens * a.group;
+      auto part = [&](int k) -> size_t {
+        return ((static_cast<size_t>(k) * a.tiles + tile) * 2 + (k == k0 ? slot0 : 0)) * a.part_rows + row;
+      };
+      float m = ninf, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      // the reference of the row: the largest of the pieces'
+      for (int k = k0 + lane; k <= k1; k += 32) m = fmaxf(m, a.part_ml[part(k)].x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float m_use = m == ninf ? 0.f : m;
+      for (int k = k0 + warp; k <= k1; k += 4) {
+        const size_t p = part(k);
+        const float2 ml = a.part_ml[p];
+        const float4 x = *reinterpret_cast<const float4*>(a.part_o + p * kHeadDim + lane * 4);
+        const float w = exp2f(ml.x - m_use);  // a piece without keys: exp2(-inf) = 0
+        if (ml.x != ninf) {
+          l += w * ml.y;
+          o.x += w * x.x;
+          o.y += w * x.y;
+          o.z += w * x.z;
+          o.w += w * x.w;
+        }
+      }
+      *reinterpret_cast<float4*>(&sm_o[warp][lane * 4]) = o;
+      if (lane == 0) sm_ml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (warp == 0) {
+        l = (sm_ml[0].y + sm_ml[1].y) + (sm_ml[2].y + sm_ml[3].y);
+        float acc[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[e] = (sm_o[0][lane * 4 + e] + sm_o[1][lane * 4 + e]) + (sm_o[2][lane * 4 + e] + sm_o[3][lane * 4 + e]);
+        float inv = l != 0.f ? 1.f / l : 0.f;
+        if (a.v_scale != nullptr) inv *= __ldg(a.v_scale + hk);
+        const int h = hk * a.group + r % a.group;
+        const size_t tok = static_cast<size_t>(q.tok0) + i;
+        uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) +
+                                              (tok * a.hq + h) * static_cast<size_t>(kHeadDim) * 2);
+        dst[lane] = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        if (lane == 0)
+          a.lse[static_cast<size_t>(h) * a.total_tokens + tok] =
+              l != 0.f ? (m_use + log2f(l)) * 0.69314718055994530942f : ninf;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <bool kFp8>
+static cudaError_t launch_tree_t(const TreeMaps& maps, const TreeArgs& args, cudaStream_t stream) {
+  const size_t smem = sizeof(TreeSmem<kFp8>);
+  static_assert(sizeof(TreeSmem<kFp8>) <= 115712, "two CTAs per SM");
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int grid = args.ranges * args.tiles;
+  tree_attn_kernel<kFp8><<<grid, TreeCfg<kFp8>::kThreads, smem, stream>>>(maps, args);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  TreeArgs j = args;
+  if (!kFp8) j.v_scale = nullptr;
+  const int most = args.max_seq_tokens < args.total_tokens ? args.max_seq_tokens : args.total_tokens;
+  const int64_t rows = static_cast<int64_t>(most) * args.group, items = static_cast<int64_t>(args.seqs) * args.hkv;
+  // nothing is cut when one range holds everything: then only the status is left
+  cudaLaunchConfig_t cfg{};
+  const int64_t gx = args.ranges > 1 ? rows : 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(args.ranges > 1 ? (items < 65535 ? items : 65535) : 1));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, tree_join_kernel, j, grid, 1);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream) {
+  return fp8 ? launch_tree_t<true>(maps, args, stream) : launch_tree_t<false>(maps, args, stream);
+}
+
+}  // namespace stem

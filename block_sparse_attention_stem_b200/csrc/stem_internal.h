@@ -17,6 +17,8 @@ namespace stem {
 // Must equal the stem_status_t values of include/stem.h.
 constexpr int STEM_ERR_TIMEOUT_CODE = 6;
 constexpr int STEM_ERR_BAD_BLOCKLIST_CODE = 7;
+constexpr int STEM_ERR_BAD_INPUT_CODE = 8;
+constexpr int STEM_ERR_OUT_OF_PAGES_CODE = 9;
 
 constexpr int kBlock = 128;      // block (tokens); also the attention's query tile for 64-token blocks
 constexpr int kMaxBitmapBlocks = 32768;  // 64-token blocks: longest sequence in blocks (2,097,152 tokens)

@@ -105,6 +105,73 @@ cudaError_t launch_vwiden(const void* v8, uint16_t* v16, int total_tokens, int h
                           const int32_t* cu_seqlens, int num_seqs, const int32_t* page_table, int page_size,
                           int num_pages, int max_pages, cudaStream_t stream);
 
+// ---- the paged cache (k_cache_extend.cu, k_rope.cu, k_tree_attn.cu)
+
+// 3-D maps of a whole [rows, heads, 128] page pool (box: box_rows rows of one
+// head) and of [tokens, heads, 128] queries (box: box_heads heads of
+// box_tokens tokens, token-major), 128-byte swizzle, one 128-byte slab wide.
+bool encode_pool_map(CUtensorMap* m, const void* base, bool fp8, int heads, int rows, int box_rows);
+bool encode_query_map(CUtensorMap* m, const void* base, bool fp8, int heads, int tokens, int box_heads,
+                      int box_tokens);
+
+constexpr int kMaxExtendSeqs = 8192;  // sequences of one stem_cache_extend (16 B of SMEM each)
+struct ExtendArgs {
+  int seqs, max_tokens, page_size, num_pages, max_pages, num_free, mask_words;
+  const int32_t *cache_lens, *new_lens, *held, *free_pages, *cursor, *parents;
+  int32_t *page_table, *held_out, *cursor_out, *cu_seqlens, *kv_lens, *slots, *positions;
+  uint32_t* mask;
+  int* status;
+};
+cudaError_t launch_cache_extend(const ExtendArgs& args, cudaStream_t stream);
+
+struct RopeArgs {
+  uint64_t turn[kHeadDim / 2];  // angular frequency of pair j in 2^-64 turns per position
+  float amplitude;
+  int rotary_dim;
+  int tokens;
+  int hq, hkv;                  // head rows of q and k to rotate (0: that tensor is not asked for)
+  int hkv_rows;                 // KV heads of a token
+  int has_v;
+  const int32_t *positions, *slots;
+  const uint8_t *q, *k, *v;     // bf16 rows
+  int64_t q_stride, k_stride, v_stride;  // bytes between tokens
+  const float *q_scale, *k_scale, *v_scale;
+  uint8_t *q_out, *k_out, *v_out, *k_pages, *v_pages;
+  int pool_rows;
+};
+cudaError_t launch_rope(const RopeArgs& args, bool interleaved, bool fp8, cudaStream_t stream);
+
+struct TreeMaps {
+  CUtensorMap q;       // box: the group's query heads of tile_tokens tokens
+  CUtensorMap k_pool;  // the page pool as [pages * page_size] rows, boxes of 64
+  CUtensorMap v_pool;
+};
+struct TreeArgs {
+  int seqs, total_tokens, max_seq_tokens, hq, hkv;
+  int group;            // query heads per KV head
+  int tile_tokens;      // tokens of a 128-row query tile
+  int box_rows;         // rows of the Q box (tile_tokens, or the longest sequence's tokens, times group)
+  int tiles;            // query tiles of the longest sequence: CTAs that share a range of keys
+  int ranges;           // ranges of keys at most (the grid is ranges * tiles)
+  int part_rows;        // rows of a partial result in the workspace
+  int page_size, num_pages, max_pages, mask_words;
+  const int32_t *cu_seqlens, *kv_lens, *page_table;
+  const uint32_t* mask;
+  float scale_log2;
+  const float *q_scale, *k_scale, *v_scale;
+  const uint8_t* v_pages;
+  void* out;
+  float* lse;
+  // workspace
+  int* status;
+  int* cta_status;      // [grid]
+  int64_t* unit0;       // [seqs + 1]: 64-key units (times KV heads) before each sequence
+  float2* part_ml;      // [grid][2][part_rows]: reference max and sum
+  float* part_o;        // [grid][2][part_rows][128]
+};
+constexpr int kTreeRanges = 296;  // two CTAs on each of 148 SMs
+cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
+
 size_t score_smem_bytes();
 size_t bsa_smem_bytes(bool fp8);
 

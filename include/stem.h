@@ -64,8 +64,11 @@ typedef enum {
   STEM_ERR_MISALIGNED = 4,           /* a tensor base pointer is not 16-byte aligned */
   STEM_ERR_CUDA = 5,                 /* a CUDA runtime/driver call failed (launch, tensor-map encode) */
   STEM_ERR_TIMEOUT = 6,              /* device: a pipeline wait exceeded its bound; outputs are invalid */
-  STEM_ERR_BAD_BLOCKLIST = 7         /* device: a CSR entry was out of range or not strictly ascending;
+  STEM_ERR_BAD_BLOCKLIST = 7,        /* device: a CSR entry was out of range or not strictly ascending;
                                         the offending entry was skipped */
+  STEM_ERR_BAD_INPUT = 8,            /* device: a length, offset, page number or parent read from device
+                                        memory was out of range (what the call then did is at the call) */
+  STEM_ERR_OUT_OF_PAGES = 9          /* device: the free list, or a row of the page table, was too short */
 } stem_status_t;
 
 typedef enum { STEM_BF16 = 0, STEM_FP8_E4M3 = 1 } stem_dtype_t;
@@ -325,6 +328,184 @@ STEM_API stem_status_t stem_prefill_noalloc(const stem_qkv_t* qkv, const stem_pa
  * Returns STEM_ERR_INVALID_ARG for a NULL `out` or a stream of another device,
  * STEM_ERR_CUDA if the copy fails. */
 STEM_API stem_status_t stem_noalloc_read_device_status(stem_stream_t stream, stem_status_t* out);
+
+/* ------------------------------------------------------------------------
+ * The paged cache after (and around) the prefill: making room and maps for a
+ * step's tokens, rotating and storing them, and answering from the cache.
+ * The pages have no counterpart (they end at the prefill layer); the page
+ * layout is stem_paged_kv_t's, so stem_bsa_fwd_paged reads the same pages.
+ * Lengths live on the device, so a captured step can be replayed while they
+ * grow.
+ * ------------------------------------------------------------------------ */
+
+/* One step of num_seqs sequences: sequence s has cache_lens[s] tokens in the
+ * cache and adds new_lens[s].  All pointers are device pointers. */
+typedef struct {
+  int32_t num_seqs;           /* S, 1 .. 8192 (STEM_ERR_UNSUPPORTED beyond) */
+  int32_t max_tokens;         /* length of the per-token outputs; >= the sum of new_lens */
+  int32_t page_size;          /* tokens per page; a multiple of 64 */
+  int32_t num_pages;          /* pages in the pool (num_pages * page_size < 2^31) */
+  int32_t max_pages_per_seq;  /* row length of the page table (S * max_pages_per_seq < 2^31) */
+  int32_t num_free;           /* length of free_pages */
+  int32_t mask_words;         /* with parents: 32-bit words per token of the mask, >= 1 */
+  const int32_t* cache_lens;  /* [S] */
+  const int32_t* new_lens;    /* [S] */
+  const int32_t* held_pages;  /* [S]: leading entries of each table row that hold a page.  More than
+                                 the cached tokens need is fine (drafts of an earlier step were
+                                 rejected): those pages are used before new ones are taken */
+  const int32_t* free_pages;  /* [num_free] page numbers, taken in order */
+  const int32_t* cursor;      /* [1]: entries of free_pages already taken */
+  const int32_t* parents;     /* [max_tokens], packed like the new tokens, or NULL (each token follows
+                                 the one before it).  The parent of a drafted token is the index,
+                                 among its sequence's new tokens, of the token it follows: below its
+                                 own index, or -1 for one that follows the cached tokens directly */
+} stem_cache_step_t;
+
+/* Extend every sequence's row of the page table by the pages that its new
+ * tokens need, and write the maps of the step:
+ *   c = cache_lens[s], n = new_lens[s], need = ceil((c + n) / page_size)
+ *   page_table [S][max_pages_per_seq] (in and out): entries held_pages[s] ..
+ *            need - 1 are filled from the free list, sequence by sequence;
+ *            every other entry is left as it was
+ *   held_out [S]   max(held_pages[s], need);  cursor_out [1] the list's new position
+ *   cu_seqlens [S + 1]   packed offsets of the new tokens;  kv_lens [S]  c + n
+ *   slots [max_tokens]   row of the pool of each new token: page * page_size + offset
+ *   positions [max_tokens]  c + i for token i, or with parents c + its number of ancestors
+ *   mask [max_tokens][mask_words] (with parents; else NULL): bit j of token i's row
+ *            is set when j is i or an ancestor of i (j, i: indices in the sequence)
+ * Entries of slots behind the last token are -1, of positions and mask 0.
+ * held_out may be held_pages, cursor_out may be cursor and kv_lens may be
+ * cache_lens (so a captured step can advance its own state); no other output
+ * may overlap an input.
+ * Device status (word at `ws`, >= 256 bytes): STEM_ERR_OUT_OF_PAGES when the
+ * free list or a table row was too short (the tokens without a page get slot
+ * -1, table entries without a page -1, held_out counts the pages obtained);
+ * STEM_ERR_BAD_INPUT for a negative length (taken as 0), held_pages outside
+ * 0 .. max_pages_per_seq or cursor outside 0 .. num_free (clamped), more than
+ * max_tokens new tokens (those beyond are dropped from every output), a page
+ * number outside the pool (slot -1), a parent not below its token (taken as
+ * -1) or a token whose mask does not fit mask_words (its bits beyond are
+ * dropped).  Nothing outside the arrays is read or written in any case.
+ * One launch; host-side STEM_ERR_INVALID_ARG for sizes and NULL pointers. */
+STEM_API stem_status_t stem_cache_extend(const stem_cache_step_t* step, int32_t* page_table, int32_t* held_out,
+                                         int32_t* cursor_out, int32_t* cu_seqlens, int32_t* kv_lens, int32_t* slots,
+                                         int32_t* positions, uint32_t* mask, void* ws, size_t ws_bytes,
+                                         stem_stream_t stream);
+
+/* Which elements of a head's rotated part form pair j (0 <= j < rotary_dim / 2). */
+typedef enum {
+  STEM_ROPE_HALF = 0,        /* (j, j + rotary_dim / 2) */
+  STEM_ROPE_INTERLEAVED = 1  /* (2 j, 2 j + 1) */
+} stem_rope_layout_t;
+
+/* Frequencies for contexts longer than the trained one (r = rotary_dim). */
+typedef enum {
+  STEM_ROPE_PLAIN = 0,   /* w_j = base^(-2 j / r) */
+  STEM_ROPE_LINEAR = 1,  /* w_j / factor (position interpolation) */
+  STEM_ROPE_NTK = 2,     /* w_j from the base base * factor^(r / (r - 2)) */
+  STEM_ROPE_YARN = 3     /* w_j (1 - t_j) + w_j / factor t_j with t_j rising from 0 at the pair that makes
+                            beta_fast turns over original_len tokens (rounded down) to 1 at the one that
+                            makes beta_slow (rounded up); amplitude 0.1 ln(factor) + 1 */
+} stem_rope_scaling_t;
+
+typedef struct {
+  int32_t layout;        /* stem_rope_layout_t */
+  int32_t rotary_dim;    /* r: the first r elements of a head are rotated, the others copied; a multiple
+                            of 16 up to head_dim (STEM_ERR_UNSUPPORTED for other even values) */
+  int32_t scaling;       /* stem_rope_scaling_t */
+  int32_t original_len;  /* YARN: trained context length, >= 1 */
+  double  base;          /* > 1 */
+  double  factor;        /* >= 1 (ignored by PLAIN) */
+  double  beta_fast;     /* YARN [32]; > beta_slow */
+  double  beta_slow;     /* YARN [1]; > 0 */
+  double  amplitude;     /* cos and sin are multiplied by this; 0 selects 1 (YARN: 0.1 ln(factor) + 1) */
+} stem_rope_t;
+
+/* Tokens to rotate: bf16 rows as a (fused) projection leaves them.  Heads of a
+ * token are contiguous; *_stride is the distance between tokens in elements (a
+ * multiple of 8, >= heads * head_dim).  Every pointer is a device pointer,
+ * 16-byte aligned (positions, slots and scales 4-byte). */
+typedef struct {
+  int32_t num_tokens;        /* T >= 0 */
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;          /* 128 */
+  int32_t out_dtype;         /* stem_dtype_t of every output and of the pages */
+  const int32_t* positions;  /* [T]; any int32 */
+  const int32_t* slots;      /* [T] with a cache: row of the pool, -1 (or any row outside the pool) to
+                                skip the token; no row may occur twice */
+  const void* q;             /* NULL with q_out NULL */
+  const void* k;             /* NULL with k_out NULL and no cache */
+  const void* v;             /* NULL with v_out NULL and no cache */
+  int64_t q_stride, k_stride, v_stride;
+  const float* q_scale;      /* e4m3 outputs: device [Hq], > 0 (stored value = e4m3(x * (1 / scale)), saturated) */
+  const float* k_scale;      /* [Hkv] */
+  const float* v_scale;      /* [Hkv] */
+  void* q_out;               /* [T, Hq, d] packed, or NULL */
+  void* k_out;               /* [T, Hkv, d] packed, or NULL */
+  void* v_out;               /* [T, Hkv, d] packed, or NULL */
+} stem_rope_io_t;
+
+/* Rotary positions for q and k, and the step's K and V into the cache.
+ * Pair (x, y) at position p becomes a (x cos(p w) - y sin(p w), y cos(p w) +
+ * x sin(p w)), a the amplitude, computed in fp32 from an angle that is reduced
+ * exactly (p w in 2^-64 turns), and rounded once to out_dtype.  v is only
+ * stored (bf16 bits kept).  q_out packed in e4m3 or bf16 feeds stem_prefill,
+ * k_out and v_out too; with `cache` (its page_table is not used and may be
+ * NULL) rows of k and v go to k_pages and v_pages at `slots`.  In place
+ * (q_out = q, k_out = k) is allowed for bf16 when the input is packed too;
+ * otherwise outputs must not overlap inputs.  A position < 0 rotates the
+ * other way.  One launch, no workspace, no device status. */
+STEM_API stem_status_t stem_rope(const stem_rope_t* rope, const stem_rope_io_t* io, const stem_paged_kv_t* cache,
+                                 stem_stream_t stream);
+
+/* Queries of one step over the paged cache.  Sequence s has the queries
+ * cu_seqlens[s] .. cu_seqlens[s + 1] - 1, whose own K and V are the last keys
+ * of its kv_lens[s] cached ones (n of them; n = 1 is plain decoding). */
+typedef struct {
+  int32_t dtype;              /* stem_dtype_t of q and of the pages */
+  int32_t num_seqs;           /* >= 1 */
+  int32_t total_tokens;       /* rows of q, out and lse: >= cu_seqlens[num_seqs] */
+  int32_t max_seq_tokens;     /* no sequence has more queries than this; 0 selects total_tokens */
+  int32_t num_q_heads;        /* Hq, a multiple of Hkv, at most 128 Hkv */
+  int32_t num_kv_heads;
+  int32_t head_dim;           /* 128 */
+  int32_t mask_words;         /* words per row of mask */
+  const int32_t* cu_seqlens;  /* device [num_seqs + 1] */
+  const int32_t* kv_lens;     /* device [num_seqs] */
+  const uint32_t* mask;       /* device [total_tokens][mask_words]: query i of a sequence sees new token j when
+                                 bit j % 32 of word j / 32 of its row is set (no bit: not seen); NULL: j <= i */
+  const void* q;              /* [T, Hq, d] */
+  const float* q_scale;       /* fp8 only, as stem_qkv_t, > 0 */
+  const float* k_scale;
+  const float* v_scale;
+  double softmax_scale;       /* 0 selects 1/sqrt(head_dim) */
+} stem_tree_t;
+
+/* Workspace bytes of stem_tree_attn for this description (host only; reads
+ * sizes, no pointers; never shrinks when num_seqs, total_tokens or
+ * max_seq_tokens grow). */
+STEM_API stem_status_t stem_tree_plan(const stem_tree_t* tree, size_t* ws_bytes);
+
+/* Attention of drafted trees, single tokens or causal chunks over the paged
+ * cache (no counterpart in the pages).
+ *   For query i of sequence s: keys u < kv_lens[s] - n, and kv_lens[s] - n + j
+ *   for every new token j it sees (one that is not in the cache because
+ *   kv_lens[s] < n - j is not there to see).
+ *   out[t][h] = sum softmax(sigma q_t . k_u) v_u,  lse[h][t] = ln sum exp(sigma q_t . k_u)
+ * out bf16 [T, Hq, d]; lse fp32 [Hq][T].  A query that sees no key gives out = 0
+ * and lse = -inf.  Rows of out and lse that belong to no sequence are left as
+ * they were.  K and V of keys that a query does not see may hold anything,
+ * infinities and NaN included, and so may rows of pages behind kv_lens[s].  A
+ * page number outside the pool reads zeros.  The work is split over the keys by
+ * the lengths alone, so the result of a call is the same bits every time.
+ * Device status: STEM_ERR_BAD_INPUT for offsets that decrease or leave 0 ..
+ * total_tokens (the sequence is skipped), a sequence with more than
+ * max_seq_tokens queries (those beyond are skipped), a negative kv_lens (taken
+ * as 0) or one past the table's row (the keys beyond are not seen);
+ * STEM_ERR_TIMEOUT.  Two launches; the workspace holds nothing between calls. */
+STEM_API stem_status_t stem_tree_attn(const stem_tree_t* tree, const stem_paged_kv_t* kv, void* out, float* lse,
+                                      void* ws, size_t ws_bytes, stem_stream_t stream);
 
 /* Self-test of the device-side failure detection (no counterpart in the
  * pages).  Launches one kernel that waits, through the same bounded wait the

@@ -1,0 +1,398 @@
+"""stem_tree_attn on the GPU against the fp64 oracle.
+
+Bounds of one output element, with A = sum p |v| / sum p, L the number of keys and
+e = (128 + 8) 2^-24 max sigma |q|.|k| the error of a logit (128 products summed in
+fp32, and its scaling):
+  * a weight is off by e (twice: its own logit and the normalisation), exp2 by
+    2^-21, and P by 2^-15 (two bf16: the first cut off below p, the rest, at
+    most 2^-7 p, rounded) or, e4m3 inputs, 2^-11 (f16; below its normal
+    range 2^-25 absolute, against weights whose largest is at least 1/2);
+  * the sums of L weights and products in fp32 by L 2^-24 each;
+  * out rounds to bf16: 2^-8 |o|.
+lse: e, L 2^-24, 2^-20 for exp2 and log2, and 2^-22 |lse| for its own arithmetic."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_oracle as C
+from oracle import stem_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+b = pytest.importorskip("block_sparse_attention_stem_b200.binding")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+
+class Case:
+    """Random queries, pages and masks of given lengths; unused pool rows are NaN."""
+
+    def __init__(self, new, ctx, hq, hkv, fp8=False, ps=64, tree=False, words=None, seed=0, extra=0, scale=0.0, spread=1.0):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator("cuda").manual_seed(seed)
+        self.new, self.kv, self.hq, self.hkv, self.fp8, self.ps, self.scale = new, [c + n for c, n in zip(ctx, new)], hq, hkv, fp8, ps, scale
+        S, T = len(new), sum(new) + extra
+        self.T, self.cu = T, [0] + list(np.cumsum(new))
+        npg = [-(-k // ps) for k in self.kv]
+        P = sum(npg) + 2
+        order = rng.permutation(P)
+        self.table = np.full((S, max(max(npg), 1) + 1), -1, dtype=np.int32)
+        o = 0
+        for s in range(S):
+            self.table[s, :npg[s]] = order[o:o + npg[s]]
+            o += npg[s]
+        used = torch.zeros(P * ps, dtype=torch.bool, device="cuda")
+        for s in range(S):
+            used[self.rows(s)] = True
+        self.qs = self.ks = self.vs = None
+        if fp8:
+            self.qs, self.ks, self.vs = (torch.rand(h, generator=g, device="cuda") * 0.01 + 0.005 for h in (hq, hkv, hkv))
+        self.q = self._enc(torch.randn(T, hq, 128, generator=g, device="cuda") * spread, self.qs)
+        self.k, self.v = (self._enc(torch.randn(P * ps, hkv, 128, generator=g, device="cuda"), sc).view(P, ps, hkv, 128)
+                          for sc in (self.ks, self.vs))
+        nan = 0x7F if fp8 else float("nan")
+        for x in (self.k, self.v):
+            x.view(P * ps, hkv, 128)[~used] = nan
+        self.mask = None
+        if tree:
+            words = words or -(-max(new) // 32)
+            m = np.zeros((T, words), dtype=np.uint32)
+            for s in range(S):
+                for i in range(new[s]):
+                    row = m[self.cu[s] + i]
+                    if i and i % 7:  # an ancestor's row and the token itself; every seventh starts afresh
+                        row |= m[self.cu[s] + int(rng.integers(max(0, i - 4), i))]
+                    if i // 32 < words:
+                        row[i // 32] |= np.uint32(1 << (i % 32))
+            self.mask = m
+
+    def _enc(self, x, sc):
+        if not self.fp8:
+            return x.to(torch.bfloat16)
+        return (x / sc[None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+    def rows(self, s):
+        u = np.arange(self.kv[s])
+        return torch.from_numpy(self.table[s, u // self.ps].astype(np.int64) * self.ps + u % self.ps).cuda()
+
+    def f64(self, x, sc):
+        if not self.fp8:
+            return x.double().cpu().numpy()
+        return O.e4m3_bytes_to_f64(x.cpu().numpy()) * sc.double().cpu().numpy()[None, :, None]
+
+    def oracle(self):
+        kr, vr = ([self.f64(x.view(-1, self.hkv, 128)[self.rows(s)], sc) for s in range(len(self.new))]
+                  for x, sc in ((self.k, self.ks), (self.v, self.vs)))
+        return C.tree_attn(self.f64(self.q, self.qs), kr, vr, self.cu, self.kv, self.mask, self.scale)
+
+    def gpu(self, max_seq_tokens=None, out=None, lse=None, ws=None, stream=None, tree=None):
+        i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()  # noqa: E731
+        self.cache = b.paged_kv(self.k, self.v, i32(self.table), self.ps)
+        self.tree = b.make_tree(self.q, i32(self.cu), i32(self.kv), self.hkv,
+                                mask=None if self.mask is None else i32(self.mask.view(np.int32)),
+                                max_seq_tokens=max(self.new) if max_seq_tokens is None else max_seq_tokens,
+                                q_scale=self.qs, k_scale=self.ks, v_scale=self.vs, softmax_scale=self.scale)
+        out, lse, ws = b.stem_tree_attn(self.tree, self.cache, out=out, lse=lse, ws=ws, stream=stream)
+        return out, lse, b.stem_read_device_status(ws, stream)
+
+    def check(self, status=0, **kw):
+        out, lse, st = self.gpu(**kw)
+        assert st == status
+        o, z, e = self.oracle()
+        n = self.cu[-1]
+        out, lse = out[:n].double().cpu().numpy(), lse[:, :n].double().cpu().numpy()
+        assert np.array_equal(np.isneginf(lse), np.isneginf(z[:, :n]))
+        L = max(self.kv)
+        logit = 136 * 2.0 ** -24 * e["qk"][:n]
+        w = 2 * logit + 2.0 ** -20 + (2.0 ** -10 if self.fp8 else 2.0 ** -15) + 2 * L * 2.0 ** -24
+        tol = 2.0 ** -8 * np.abs(o[:n]) + w[..., None] * e["absav"][:n] + 1e-30
+        if self.fp8:
+            tol += (2 * L * 2.0 ** -25 * e["vmax"][:n])[..., None]
+        assert np.all(np.abs(out - o[:n]) <= tol), float((np.abs(out - o[:n]) / tol).max())
+        see = ~np.isneginf(lse)
+        lz, zz = np.where(see, lse, 0), np.where(see, z[:, :n], 0)
+        assert np.all(np.abs(lz - zz) <= logit.T + L * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * np.abs(zz))
+        assert np.all(out[~see.T] == 0)
+        return out, lse
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ctx", [0, 1, 62, 63, 64, 127, 128, 300, 1000, 5001])
+def test_single_tokens(ctx, fp8):
+    Case([1], [ctx], 8, 2, fp8, seed=ctx).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 2), (3, 1), (6, 2), (20, 4), (8, 1), (33, 1), (64, 1), (65, 1), (128, 1)])
+def test_head_layouts(hq, hkv, fp8):
+    Case([3, 1], [200, 77], hq, hkv, fp8, seed=hq).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,ctx", [(2, 0), (5, 60), (16, 48), (31, 33), (32, 1000), (33, 127), (63, 1), (64, 640),
+                                   (65, 64), (100, 30), (256, 100)])
+def test_trees(n, ctx, fp8):
+    Case([n], [ctx], 4, 1, fp8, tree=True, seed=n).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,ctx", [(2, 0), (64, 0), (65, 3), (200, 500), (700, 129)])
+def test_causal_chunks(n, ctx, fp8):
+    Case([n], [ctx], 3, 1, fp8, seed=n).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ps", [64, 128, 192, 256])
+def test_ragged_batches_and_page_sizes(ps, fp8):
+    Case([1, 7, 0, 33, 2, 12, 1], [900, 0, 50, 63, 64, 1500, 191], 8, 2, fp8, ps=ps, tree=True, seed=ps).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_short_sequences(fp8):
+    """Items of one unit, several per range, and more sequences than threads."""
+    rng = np.random.default_rng(3)
+    new = [int(x) for x in rng.integers(0, 3, 700)]
+    new[17] = 40  # Q tiles of more than 64 rows have a single buffer
+    Case(new, [int(x) for x in rng.integers(0, 70, 700)], 4, 2, fp8, seed=3).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_unit_items_with_full_tiles(fp8):
+    """Many items of one unit whose Q tile fills the single buffer."""
+    S = 400
+    Case([32] * S, [0, 20, 32, 5] * (S // 4), 8, 2, fp8, tree=True, seed=4).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_large_logits(fp8):
+    """The running reference moves often, and weights underflow."""
+    Case([5, 1], [2000, 3000], 4, 2, fp8, seed=8, spread=12.0).check()
+    Case([5, 1], [2000, 3000], 4, 2, fp8, seed=9, scale=1.5).check()
+
+
+def test_more_tiles_than_ranges():
+    c = Case([9700], [30], 4, 1, seed=10)
+    out, lse, st = c.gpu()
+    assert st == 0
+    k = c.f64(c.k.view(-1, 1, 128)[c.rows(0)], None)
+    v = c.f64(c.v.view(-1, 1, 128)[c.rows(0)], None)
+    q = c.f64(c.q, None)
+    for t in (0, 1, 31, 32, 5000, 9699):
+        L = 30 + t + 1
+        o, z, e = C.tree_attn(q[t:t + 1], [k[:L]], [v[:L]], [0, 1], [L])
+        logit = 136 * 2.0 ** -24 * e["qk"]
+        tol = 2.0 ** -8 * np.abs(o) + (2 * logit + 2.0 ** -14 + 2 * L * 2.0 ** -24)[..., None] * e["absav"]
+        assert np.all(np.abs(out[t].double().cpu().numpy() - o[0]) <= tol[0])
+        assert np.all(np.abs(lse[:, t].double().cpu().numpy() - z[:, 0]) <= logit[0] + L * 2.0 ** -24 + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_context_split_over_all_ranges(fp8):
+    Case([4], [70000], 4, 1, fp8, tree=True, seed=11).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_whose_mask_leaves_nothing(fp8):
+    c = Case([6, 40], [0, 0], 4, 2, fp8, tree=True, seed=12)
+    c.mask[[1, 4, 9, 45]] = 0
+    out, lse = c.check()
+    assert np.all(np.isneginf(lse[:, [1, 4, 9, 45]])) and np.all(out[[1, 4, 9, 45]] == 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_queries_without_any_key(fp8):
+    c = Case([3, 2], [10, 5], 4, 2, fp8, seed=13)
+    c.kv[1] = 0
+    out, lse = c.check()
+    assert np.all(np.isneginf(lse[:, 3:])) and np.all(out[3:] == 0)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_new_tokens_that_are_not_in_the_cache(tree):
+    """kv_lens below the number of queries: the first new tokens have no key."""
+    c = Case([9], [20], 4, 2, tree=tree, seed=14)
+    c.kv[0] = 4
+    c.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,ctx", [(12, 100), (40, 0), (70, 61), (5, 64)])
+def test_nan_and_infinity_behind_the_mask(n, ctx, fp8):
+    """Hidden tokens of a tree hold NaN and infinities in K and V: only the rows that see them are touched."""
+    c = Case([n, 1], [ctx, 30], 4, 2, fp8, tree=True, seed=15)
+    rows = c.rows(0)
+    bad = [ctx + n - 1, ctx + n // 2]
+    hidden = [i for i in range(n) if not any(C.sees(i, u - ctx, c.mask[i]) for u in bad)]
+    ref, zref, e = c.oracle()
+    k, v = c.k.view(-1, 2, 128), c.v.view(-1, 2, 128)
+    nan, inf = (0x7F, 0xFF) if fp8 else (float("nan"), float("inf"))
+    k[rows[bad[0]], 0, 3], v[rows[bad[0]], :, ::5] = nan, nan
+    v[rows[bad[1]], 1, 7] = inf
+    out, lse, st = c.gpu()
+    assert st == 0 and len(hidden) > 0
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    clean = hidden + [n]
+    assert np.all(np.isfinite(out[clean])) and np.all(np.isfinite(lse[:, clean]))
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * e["absav"]
+    assert np.all(np.abs(out - ref)[clean] <= tol[clean])
+    i = n - 1  # sees itself
+    assert np.all(np.isnan(out[i][:2])) and np.all(np.isnan(out[i, 2:, ::5]))  # KV head 0: its logits are NaN
+    rest = np.ones(128, dtype=bool)
+    rest[::5] = False
+    if not C.sees(i, bad[1] - ctx, c.mask[i]):
+        assert np.all(np.isfinite(out[i, 2:][:, rest]))
+    j = bad[1] - ctx
+    if not C.sees(j, bad[0] - ctx, c.mask[j]):
+        got = out[j, 2:, 7]
+        assert np.all(np.isnan(got) if fp8 else np.isposinf(got))
+        rest = np.arange(128) != 7
+        assert np.all(np.abs(out - ref)[j][2:][:, rest] <= tol[j][2:][:, rest])
+
+
+def test_infinity_in_a_cached_value_is_everyones():
+    c = Case([3], [500], 4, 2, seed=16)
+    c.v.view(-1, 2, 128)[c.rows(0)[100], 1, 9] = float("inf")
+    out, _, _ = c.gpu()
+    assert torch.isinf(out[:, 2:, 9]).all() and torch.isfinite(out[:, :2]).all()
+
+
+def test_pages_outside_the_pool_read_zeros():
+    c = Case([2], [300], 4, 2, seed=17)
+    out, lse = c.check()
+    c.k.view(-1, 2, 128)[c.rows(0)[64:128]] = 0
+    c.v.view(-1, 2, 128)[c.rows(0)[64:128]] = 0
+    want, wl, _ = c.gpu()
+    for page in (-1, -2 ** 31, c.k.shape[0], 2 ** 31 - 1, 2 ** 25):
+        c.table[0, 1] = page
+        out, lse, st = c.gpu()
+        assert st == 0 and torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_two_sequences_share_pages():
+    c = Case([2, 2], [256, 256], 4, 2, seed=18)
+    c.table[1, :4] = c.table[0, :4]
+    c.check()
+
+
+def test_values_out_of_range_are_reported():
+    c = Case([2, 3, 1], [100, 50, 20], 4, 2, seed=19)
+    want, wl, _ = c.gpu()
+    fill = lambda: (torch.full_like(want, 7), torch.full_like(wl, 7))  # noqa: E731
+    # the work is cut by all lengths, so other cuts may round otherwise: each side is within
+    # 2^-8 |o| + 2^-13 sum p |v| / sum p <= 2^-8 |o| + 2^-11 of the exact value (|v| < 4 on average)
+    same = lambda x, y: torch.allclose(x.float(), y.float(), rtol=2.0 ** -7, atol=2.0 ** -10)  # noqa: E731
+    # a sequence whose offsets leave the batch, or go back, is skipped; the others are computed
+    for cu in ([0, 2, 5, 9], [0, 2, 2 ** 31 - 1, 6], [0, 2, 1, 1], [-1, 2, 5, 6]):
+        c.cu = cu
+        out, lse = fill()
+        out, lse, st = c.gpu(out=out, lse=lse)
+        assert st == 8
+        for s in range(3):
+            good = 0 <= cu[s] <= cu[s + 1] <= 6
+            if good and cu[s:s + 2] == [0, 2, 5, 6][s:s + 2]:
+                assert same(out[cu[s]:cu[s + 1]], want[cu[s]:cu[s + 1]])
+            elif not good and 0 <= cu[s] < 6:
+                assert torch.all(out[cu[s]:[2, 5, 6][s]] == 7)
+    c.cu = [0, 2, 5, 6]
+    out, lse = fill()
+    out, lse, st = c.gpu(max_seq_tokens=2, out=out, lse=lse)  # the third query of the second sequence is left out
+    assert st == 8 and torch.all(out[4] == 7) and torch.all(lse[:, 4] == 7)
+    keep = [0, 1, 2, 3, 5]
+    assert same(out[keep], want[keep]) and same(lse[:, keep], wl[:, keep])
+    c.kv[1] = -5
+    out, lse, st = c.gpu()
+    assert st == 8 and torch.all(out[2:5] == 0) and torch.isneginf(lse[:, 2:5]).all() and same(out[:2], want[:2])
+    c.kv[1] = 10 ** 9  # past the table's row: those keys are not seen
+    out, lse, st = c.gpu()
+    assert st == 8 and same(out[:2], want[:2]) and same(out[5:], want[5:])
+
+
+def test_rows_behind_the_last_sequence_are_left_as_they_were():
+    c = Case([2, 3], [100, 50], 4, 2, seed=20, extra=4)
+    out, lse = torch.full((9, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((4, 9), 5.0, device="cuda")
+    c.check(out=out, lse=lse)
+    assert torch.all(out[5:] == 5) and torch.all(lse[:, 5:] == 5)
+
+
+def test_no_queries_at_all():
+    c = Case([0, 0], [10, 0], 4, 2, seed=21, extra=3)
+    out, lse = torch.full((3, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((4, 3), 5.0, device="cuda")
+    out, lse, st = c.gpu(max_seq_tokens=1, out=out, lse=lse)
+    assert st == 0 and torch.all(out == 5) and torch.all(lse == 5)
+    c = Case([0], [10], 4, 2, seed=21)
+    out, lse, st = c.gpu(max_seq_tokens=0)
+    assert st == 0 and out.shape[0] == 0
+
+
+def test_mask_words_that_do_not_cover_the_tokens():
+    Case([50], [20], 4, 2, tree=True, words=1, seed=22).check()
+    Case([5], [20], 4, 2, tree=True, words=4, seed=22).check()
+
+
+def test_the_same_bits_every_time_and_on_another_stream():
+    c = Case([1, 20, 3], [4000, 900, 20000], 8, 2, tree=True, seed=23)
+    out, lse, _ = c.gpu()
+    for _ in range(3):
+        o2, l2, _ = c.gpu(max_seq_tokens=20)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    o2, l2, _ = c.gpu(stream=s)
+    s.synchronize()
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_captured_call_follows_growing_lengths_and_shares_its_workspace():
+    """Two captured calls on one workspace, replayed while kv_lens grows."""
+    c = Case([1, 1], [900, 60], 8, 2, seed=24)
+    d = Case([4, 2], [300, 2000], 8, 2, seed=25, fp8=True)
+    c.gpu()
+    d.gpu()
+    ws = torch.empty(max(b.stem_tree_ws_bytes(c.tree), b.stem_tree_ws_bytes(d.tree)), dtype=torch.uint8, device="cuda")
+    outs, graphs = [], []
+    for x in (c, d):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(b.stem_tree_attn(x.tree, x.cache, ws=ws)[:2])
+        graphs.append(g)
+    for grow in (0, 1, 3, 5):
+        for x, (o, z), g in zip((c, d), outs, graphs):
+            kv = x.tree.kv_lens.clone()
+            x.tree.kv_lens -= grow
+            g.replay()
+            assert b.stem_read_device_status(ws) == 0
+            o2, z2, _ = b.stem_tree_attn(x.tree, x.cache)
+            assert torch.equal(o, o2) and torch.equal(z, z2)
+            x.tree.kv_lens.copy_(kv)
+
+
+def test_two_calls_at_once_on_their_own_workspaces():
+    c = Case([30, 7], [9000, 15000], 8, 2, tree=True, seed=26)
+    out, lse, _ = c.gpu()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(b.stem_tree_attn(c.tree, c.cache))
+    torch.cuda.synchronize()
+    for o, z, _ in got:
+        assert torch.equal(o, out) and torch.equal(z, lse)
+
+
+def test_pages_past_32_bit_offsets():
+    P, hkv = 33000, 8
+    pool = [torch.zeros(P, 64, hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    g = torch.Generator("cuda").manual_seed(1)
+    pages = torch.tensor([[P - 1, 3, P - 2]], dtype=torch.int32, device="cuda")
+    for p in pool:
+        p[pages[0].long()] = torch.randn(3, 64, hkv, 128, generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn(2, 8, 128, generator=g, device="cuda").to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    tree = b.make_tree(q, torch.tensor([0, 2], **i32), torch.tensor([170], **i32), hkv, max_seq_tokens=2)
+    out, lse, _ = b.stem_tree_attn(tree, b.paged_kv(*pool, pages, 64))
+    small = [p[pages[0].long()].contiguous() for p in pool]
+    o2, l2, _ = b.stem_tree_attn(tree, b.paged_kv(*small, torch.tensor([[0, 1, 2]], **i32), 64))
+    assert torch.equal(out, o2) and torch.equal(lse, l2) and torch.isfinite(out.float()).all()
