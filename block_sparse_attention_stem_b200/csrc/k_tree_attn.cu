@@ -41,6 +41,7 @@
 //   warp  5    TMEM owner and MMA issuer    warps 6-7 (e4m3)  V -> f16
 // Every wait is bounded; on expiry all roles leave and the call reports it.
 #include "stem_bsa_common.cuh"
+#include "stem_tree_common.cuh"
 
 namespace stem {
 
@@ -49,7 +50,6 @@ namespace {
 constexpr int kUnit = 64;  // keys per S buffer
 constexpr int kProducer = 4, kMmaIssuer = 5, kWidenWarp = 6;
 constexpr uint32_t kTmemCols = 256;  // S buffers at 0 and 64, O at 128
-constexpr int kMinRange = 4;         // units below which a range is not cut further
 
 template <bool kFp8>
 struct TreeCfg {
@@ -76,146 +76,11 @@ struct TreeSmem {
   uint64_t p_full[2];   // the softmax warps stored P_h (and rescaled O)
   uint64_t pv_done[2];  // P_h V_h complete
   uint64_t drain;
-  int64_t scan[16];
-  int64_t total, skip;  // units of the call; units of the first sequence before this range
-  int first_seq;
+  RangeScratch range;
   uint32_t tmem_base;
   int status, abort;
   int odd_v[4];  // [item % 4]: item + 1 when a non-finite element of V was zeroed in it
 };
-
-// Keys and queries of one sequence, as the call sees them.
-struct SeqShape {
-  int tok0, n, rows;  // first packed token, new tokens, tokens that are computed
-  int ctx, kv;        // keys before the new tokens (negative when some are not cached), end of the keys
-  int units;          // 0: nothing to do
-  bool bad;
-};
-
-__device__ __forceinline__ SeqShape seq_shape(const TreeArgs& a, int s) {
-  SeqShape r;
-  const int t0 = __ldg(a.cu_seqlens + s), t1 = __ldg(a.cu_seqlens + s + 1);
-  const int kv = max(__ldg(a.kv_lens + s), 0);
-  const int64_t cap = i64min(static_cast<int64_t>(a.max_pages) * a.page_size, 0x7fffff80);
-  r.bad = t0 < 0 || t1 < t0 || t1 > a.total_tokens;
-  r.tok0 = t0;
-  r.n = r.bad ? 0 : t1 - t0;
-  r.rows = min(r.n, a.max_seq_tokens);
-  r.ctx = kv - r.n;
-  r.kv = kv < cap ? kv : static_cast<int>(cap);
-  r.units = r.n == 0 ? 0 : max((r.kv + kUnit - 1) / kUnit, 1);
-  if (r.n > 0) r.bad |= r.rows < r.n || kv > cap || __ldg(a.kv_lens + s) < 0;
-  return r;
-}
-
-__device__ __forceinline__ int64_t range_begin(int64_t total, int ranges, int k) { return total * k / ranges; }
-// ranges in use: none is shorter than kMinRange units
-__device__ __forceinline__ int ranges_used(int64_t total, int most) {
-  return static_cast<int>(i64max(i64min(most, total / kMinRange), 1));
-}
-
-// Walks the items (sequence, KV head) of a range; every role walks alike.
-struct Walk {
-  int s, hk, unit;  // next item and its first unit
-  int64_t left;     // units of the range from there on
-  int index;        // items seen so far
-  SeqShape q;
-  // current item
-  int hk_cur, ub, ue;
-  bool whole;
-  __device__ __forceinline__ void start(const TreeArgs& a, int first_seq, int64_t skip, int64_t count) {
-    s = first_seq;
-    left = count;
-    index = 0;
-    q.units = 0;
-    if (count > 0) {
-      q = seq_shape(a, s);
-      hk = static_cast<int>(skip / q.units);
-      unit = static_cast<int>(skip % q.units);
-    }
-  }
-  // the next item whose sequence has this tile; false at the end of the range
-  __device__ __forceinline__ bool next(const TreeArgs& a, int tile) {
-    while (left > 0) {
-      if (hk == a.hkv) {
-        hk = 0;
-        do {
-          if (++s >= a.seqs) {  // the lengths changed under the call
-            left = 0;
-            return false;
-          }
-          q = seq_shape(a, s);
-        } while (q.units == 0);
-      }
-      hk_cur = hk;
-      ub = unit;
-      ue = static_cast<int>(i64min(q.units, unit + left));
-      whole = ub == 0 && ue == q.units;
-      left -= ue - ub;
-      unit = ue;
-      if (ue == q.units) {
-        unit = 0;
-        ++hk;
-      }
-      ++index;
-      if (tile * a.tile_tokens < q.rows) return true;
-    }
-    return false;
-  }
-};
-
-// Bits of the 64 keys from `key0` on that query i of the sequence sees.
-__device__ __forceinline__ uint64_t visible(const TreeArgs& a, const SeqShape& q, int i, int key0) {
-  const int d0 = key0 - q.ctx;  // index, among the new tokens, of the first key
-  uint64_t bits;
-  if (a.mask == nullptr) {
-    const int seen = i + 1 - d0;  // new tokens up to i, from the first key on
-    bits = seen <= 0 ? 0ull : seen >= 64 ? ~0ull : (1ull << seen) - 1;
-  } else {
-    const uint32_t* row = a.mask + static_cast<size_t>(q.tok0 + i) * a.mask_words;
-    const int from = max(d0, 0);
-    const int w = from >> 5, sh = from & 31;
-    auto word = [&](int x) -> uint64_t { return x < a.mask_words ? __ldg(row + x) : 0u; };
-    const uint64_t lo = word(w) | word(w + 1) << 32;
-    bits = sh == 0 ? lo : lo >> sh | word(w + 2) << (64 - sh);
-    if (q.n - from < 64) bits &= (1ull << (q.n - from > 0 ? q.n - from : 0)) - 1;
-    if (d0 < 0) bits = (d0 > -64 ? bits << -d0 | ((1ull << -d0) - 1) : ~0ull);
-  }
-  const int keys = q.kv - key0;
-  if (keys < 64) bits &= keys <= 0 ? 0ull : (1ull << keys) - 1;
-  return bits;
-}
-
-// Pool row of key u of sequence s, or the first row past the pool (reads zeros).
-__device__ __forceinline__ int pool_row(const TreeArgs& a, int s, int u) {
-  const int pg = u / a.page_size;
-  const int page = pg < a.max_pages ? __ldg(a.page_table + static_cast<size_t>(s) * a.max_pages + pg) : -1;
-  if (page < 0 || page >= a.num_pages) return a.num_pages * a.page_size;
-  return page * a.page_size + (u - pg * a.page_size);
-}
-
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
-
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Non-finite 16-bit elements (bf16: exponent 0xff) of a pair are zeroed.
-__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& odd) {
-  if ((w & 0x7f80u) == 0x7f80u) {
-    w &= 0xffff0000u;
-    odd = true;
-  }
-  if ((w & 0x7f800000u) == 0x7f800000u) {
-    w &= 0x0000ffffu;
-    odd = true;
-  }
-  return w;
-}
 
 }  // namespace
 
@@ -236,55 +101,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
     if (sm.abort) sm.status = STEM_ERR_TIMEOUT_CODE;
     for (int x = 0; x < 4; ++x) sm.odd_v[x] = 0;
   }
-  const int per = (a.seqs + Cfg::kThreads - 1) / Cfg::kThreads;
-  const int s_beg = min(static_cast<int>(threadIdx.x) * per, a.seqs), s_end = min(s_beg + per, a.seqs);
-  int64_t mine = 0;
-  bool bad = false;
-  for (int s = s_beg; s < s_end; ++s) {
-    const SeqShape q = seq_shape(a, s);
-    mine += q.units;
-    bad |= q.bad;
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += y;
-  }
-  if (lane == 31) sm.scan[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < Cfg::kThreads / 32; ++w) {
-    if (w < warp) before += sm.scan[w];
-    total += sm.scan[w];
-  }
-  before *= a.hkv;
-  mine *= a.hkv;
-  total *= a.hkv;
-  const int used = ranges_used(total, a.ranges);
-  const int64_t u0 = range < used ? range_begin(total, used, range) : total;
-  const int64_t count = range < used ? range_begin(total, used, range + 1) - u0 : 0;
-  if (bad && blockIdx.x == 0) set_status(&sm.status, STEM_ERR_BAD_INPUT_CODE);
-  if (blockIdx.x == 0) {
-    int64_t at = before;
-    for (int s = s_beg; s < s_end; ++s) {
-      a.unit0[s] = at;
-      at += static_cast<int64_t>(seq_shape(a, s).units) * a.hkv;
-    }
-    if (threadIdx.x == 0) a.unit0[a.seqs] = total;
-  }
-  if (count > 0 && before <= u0 && u0 < before + mine) {
-    int64_t at = before;
-    int s = s_beg;
-    for (;; ++s) {
-      const int64_t more = static_cast<int64_t>(seq_shape(a, s).units) * a.hkv;
-      if (u0 < at + more) break;
-      at += more;
-    }
-    sm.first_seq = s;
-    sm.skip = u0 - at;
-  }
+  const int64_t count = find_range<Cfg::kThreads>(a, range, sm.range, &sm.status);
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.q_full[b], 1);
@@ -321,7 +138,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
   volatile int* abort = &sm.abort;
   int* status = &sm.status;
   Walk wk;
-  wk.start(a, sm.first_seq, sm.skip, count);
+  wk.start(a, sm.range.first_seq, sm.range.skip, count);
   // Q tiles of at most 64 rows have two buffers, so that the next item's
   // products need not wait for the last one's
   const int qbufs = a.box_rows <= 64 ? 2 : 1;
@@ -809,7 +626,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
     const int64_t units = (a.unit0[s + 1] - at) / a.hkv;
     if (units == 0) continue;
     const int64_t total = a.unit0[a.seqs];
-    const int used = ranges_used(total, a.ranges);
+    const int used = ranges_used(a, total);
     const int64_t first = at + hk * units, last = first + units - 1;
     // the range that holds unit x: the largest k with range_begin(k) <= x
     const int k0 = static_cast<int>(((first + 1) * used - 1) / total);
@@ -877,8 +694,13 @@ static cudaError_t launch_tree_t(const TreeMaps& maps, const TreeArgs& args, cud
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int grid = args.ranges * args.tiles;
-  tree_attn_kernel<kFp8><<<grid, TreeCfg<kFp8>::kThreads, smem, stream>>>(maps, args);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (args.unit_keys == kUnit) {
+    tree_attn_kernel<kFp8><<<grid, TreeCfg<kFp8>::kThreads, smem, stream>>>(maps, args);
+    e = cudaGetLastError();
+  } else {
+    e = launch_tree_narrow(maps, args, kFp8, stream);
+  }
+  if (e != cudaSuccess) return e;
   TreeArgs j = args;
   if (!kFp8) j.v_scale = nullptr;
   const int most = args.max_seq_tokens < args.total_tokens ? args.max_seq_tokens : args.total_tokens;

@@ -154,6 +154,7 @@ struct TreeArgs {
   int tiles;            // query tiles of the longest sequence: CTAs that share a range of keys
   int ranges;           // ranges of keys at most (the grid is ranges * tiles)
   int part_rows;        // rows of a partial result in the workspace
+  int unit_keys;        // keys of a unit: 64, or 128 in the narrow kernel
   int page_size, num_pages, max_pages, mask_words;
   const int32_t *cu_seqlens, *kv_lens, *page_table;
   const uint32_t* mask;
@@ -169,8 +170,11 @@ struct TreeArgs {
   float2* part_ml;      // [grid][2][part_rows]: reference max and sum
   float* part_o;        // [grid][2][part_rows][128]
 };
-constexpr int kTreeRanges = 296;  // two CTAs on each of 148 SMs
+constexpr int kTreeRanges = 296;    // two CTAs on each of 148 SMs
+constexpr int kNarrowRanges = 148;  // one CTA per SM
+constexpr int kNarrowRows = 32;     // query rows (tokens * group) up to which the narrow kernel is used
 cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
+cudaError_t launch_tree_narrow(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
 
 size_t score_smem_bytes();
 size_t bsa_smem_bytes(bool fp8);

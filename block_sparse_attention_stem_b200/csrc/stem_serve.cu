@@ -98,7 +98,7 @@ stem_status_t check_rows(const void* in, int64_t stride, int heads, const void* 
 }
 
 struct TreeLayout {
-  int group, tile_tokens, box_tokens, tiles, ranges, part_rows;
+  int group, tile_tokens, box_tokens, tiles, ranges, part_rows, unit_keys;
   size_t off_cta, off_unit0, off_ml, off_o, bytes;
 };
 
@@ -118,7 +118,9 @@ stem_status_t tree_layout(const stem_tree_t* t, TreeLayout* out) {
                                                                                 : std::max(t->total_tokens, 1);
   l.box_tokens = std::min(l.tile_tokens, most);
   l.tiles = (most + l.tile_tokens - 1) / l.tile_tokens;
-  l.ranges = std::max(kTreeRanges / l.tiles, 1);
+  const bool narrow = most <= kNarrowRows / l.group;
+  l.unit_keys = narrow ? 128 : 64;
+  l.ranges = narrow ? kNarrowRanges : std::max(kTreeRanges / l.tiles, 1);
   l.part_rows = l.ranges > 1 ? l.box_tokens * l.group : 0;  // one range: nothing is split
   const size_t grid = std::max<size_t>(static_cast<size_t>(l.ranges) * l.tiles, kTreeRanges);
   l.off_cta = kStatusBytes;
@@ -279,6 +281,7 @@ stem_status_t stem_tree_attn(const stem_tree_t* tree, const stem_paged_kv_t* kv,
   a.tiles = l.tiles;
   a.ranges = l.ranges;
   a.part_rows = l.part_rows;
+  a.unit_keys = l.unit_keys;
   a.page_size = kv->page_size;
   a.num_pages = kv->num_pages;
   a.max_pages = kv->max_pages_per_seq;

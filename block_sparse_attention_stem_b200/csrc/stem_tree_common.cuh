@@ -1,0 +1,233 @@
+// stem_tree_common.cuh — pieces shared by the kernels of attention over the
+// paged cache: the shape of a sequence, the equal cuts of the keys, the walk
+// over a range's items, masks and page lookups.
+#pragma once
+
+#include "stem_device.cuh"
+#include "stem_kernels.h"
+
+namespace stem {
+namespace {
+
+constexpr int kMinRangeKeys = 256;  // keys below which a range is not cut further
+
+// Keys and queries of one sequence, as the call sees them.
+struct SeqShape {
+  int tok0, n, rows;  // first packed token, new tokens, tokens that are computed
+  int ctx, kv;        // keys before the new tokens (negative when some are not cached), end of the keys
+  int units;          // 0: nothing to do
+  bool bad;
+};
+
+__device__ __forceinline__ SeqShape seq_shape(const TreeArgs& a, int s) {
+  SeqShape r;
+  const int t0 = __ldg(a.cu_seqlens + s), t1 = __ldg(a.cu_seqlens + s + 1);
+  const int kv = max(__ldg(a.kv_lens + s), 0);
+  const int64_t cap = i64min(static_cast<int64_t>(a.max_pages) * a.page_size, 0x7fffff80);
+  r.bad = t0 < 0 || t1 < t0 || t1 > a.total_tokens;
+  r.tok0 = t0;
+  r.n = r.bad ? 0 : t1 - t0;
+  r.rows = min(r.n, a.max_seq_tokens);
+  r.ctx = kv - r.n;
+  r.kv = kv < cap ? kv : static_cast<int>(cap);
+  r.units = r.n == 0 ? 0 : max((r.kv + a.unit_keys - 1) / a.unit_keys, 1);
+  if (r.n > 0) r.bad |= r.rows < r.n || kv > cap || __ldg(a.kv_lens + s) < 0;
+  return r;
+}
+
+__device__ __forceinline__ int64_t range_begin(int64_t total, int ranges, int k) { return total * k / ranges; }
+// ranges in use: none is shorter than kMinRangeKeys
+__device__ __forceinline__ int ranges_used(const TreeArgs& a, int64_t total) {
+  return static_cast<int>(i64max(i64min(a.ranges, total * a.unit_keys / kMinRangeKeys), 1));
+}
+
+// Walks the items (sequence, KV head) of a range; every role walks alike.
+struct Walk {
+  int s, hk, unit;  // next item and its first unit
+  int64_t left;     // units of the range from there on
+  int index;        // items seen so far
+  SeqShape q;
+  // current item
+  int hk_cur, ub, ue;
+  bool whole;
+  __device__ __forceinline__ void start(const TreeArgs& a, int first_seq, int64_t skip, int64_t count) {
+    s = first_seq;
+    left = count;
+    index = 0;
+    q.units = 0;
+    if (count > 0) {
+      q = seq_shape(a, s);
+      hk = static_cast<int>(skip / q.units);
+      unit = static_cast<int>(skip % q.units);
+    }
+  }
+  // the next item whose sequence has this tile; false at the end of the range
+  __device__ __forceinline__ bool next(const TreeArgs& a, int tile) {
+    while (left > 0) {
+      if (hk == a.hkv) {
+        hk = 0;
+        do {
+          if (++s >= a.seqs) {  // the lengths changed under the call
+            left = 0;
+            return false;
+          }
+          q = seq_shape(a, s);
+        } while (q.units == 0);
+      }
+      hk_cur = hk;
+      ub = unit;
+      ue = static_cast<int>(i64min(q.units, unit + left));
+      whole = ub == 0 && ue == q.units;
+      left -= ue - ub;
+      unit = ue;
+      if (ue == q.units) {
+        unit = 0;
+        ++hk;
+      }
+      ++index;
+      if (tile * a.tile_tokens < q.rows) return true;
+    }
+    return false;
+  }
+};
+
+// Bits of the 64 keys from `key0` on that query i of the sequence sees.
+__device__ __forceinline__ uint64_t visible(const TreeArgs& a, const SeqShape& q, int i, int key0) {
+  const int d0 = key0 - q.ctx;  // index, among the new tokens, of the first key
+  uint64_t bits;
+  if (a.mask == nullptr) {
+    const int seen = i + 1 - d0;  // new tokens up to i, from the first key on
+    bits = seen <= 0 ? 0ull : seen >= 64 ? ~0ull : (1ull << seen) - 1;
+  } else {
+    const uint32_t* row = a.mask + static_cast<size_t>(q.tok0 + i) * a.mask_words;
+    const int from = max(d0, 0);
+    const int w = from >> 5, sh = from & 31;
+    auto word = [&](int x) -> uint64_t { return x < a.mask_words ? __ldg(row + x) : 0u; };
+    const uint64_t lo = word(w) | word(w + 1) << 32;
+    bits = sh == 0 ? lo : lo >> sh | word(w + 2) << (64 - sh);
+    if (q.n - from < 64) bits &= (1ull << (q.n - from > 0 ? q.n - from : 0)) - 1;
+    if (d0 < 0) bits = (d0 > -64 ? bits << -d0 | ((1ull << -d0) - 1) : ~0ull);
+  }
+  const int keys = q.kv - key0;
+  if (keys < 64) bits &= keys <= 0 ? 0ull : (1ull << keys) - 1;
+  return bits;
+}
+
+// Pool row of key u of sequence s, or the first row past the pool (reads zeros).
+__device__ __forceinline__ int pool_row(const TreeArgs& a, int s, int u) {
+  const int pg = u / a.page_size;
+  const int page = pg < a.max_pages ? __ldg(a.page_table + static_cast<size_t>(s) * a.max_pages + pg) : -1;
+  if (page < 0 || page >= a.num_pages) return a.num_pages * a.page_size;
+  return page * a.page_size + (u - pg * a.page_size);
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// L2 cache policy for data that is read once, and the tile load that carries it.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
+// d = a * b on both halves.
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+// Non-finite bf16 elements (exponent 0xff) of a pair are zeroed.
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& odd) {
+  if ((w & 0x7f80u) == 0x7f80u) {
+    w &= 0xffff0000u;
+    odd = true;
+  }
+  if ((w & 0x7f800000u) == 0x7f800000u) {
+    w &= 0x0000ffffu;
+    odd = true;
+  }
+  return w;
+}
+
+// Where a range starts, found by all threads of the CTA (kThreads of them):
+// prefix sums of the sequences' units.
+struct RangeStart {
+  int64_t skip, count;  // units of first_seq before the range; units of the range
+  int first_seq;
+};
+struct RangeScratch {
+  int64_t scan[16];
+  int64_t skip;
+  int first_seq;
+};
+// One __syncthreads inside; the caller's next one publishes skip and first_seq
+// (count is known to every thread).  CTA 0 also writes unit0 for the joining
+// kernel and reports bad lengths.
+template <int kThreads>
+__device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, RangeScratch& sm, int* status) {
+  const int warp = warp_id(), lane = lane_id();
+  const int per = (a.seqs + kThreads - 1) / kThreads;
+  const int s_beg = min(static_cast<int>(threadIdx.x) * per, a.seqs), s_end = min(s_beg + per, a.seqs);
+  int64_t mine = 0;
+  bool bad = false;
+  for (int s = s_beg; s < s_end; ++s) {
+    const SeqShape q = seq_shape(a, s);
+    mine += q.units;
+    bad |= q.bad;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) sm.scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sm.scan[w];
+    total += sm.scan[w];
+  }
+  before *= a.hkv;
+  mine *= a.hkv;
+  total *= a.hkv;
+  const int used = ranges_used(a, total);
+  const int64_t u0 = range < used ? range_begin(total, used, range) : total;
+  const int64_t count = range < used ? range_begin(total, used, range + 1) - u0 : 0;
+  if (blockIdx.x == 0) {
+    if (bad) set_status(status, STEM_ERR_BAD_INPUT_CODE);
+    int64_t at = before;
+    for (int s = s_beg; s < s_end; ++s) {
+      a.unit0[s] = at;
+      at += static_cast<int64_t>(seq_shape(a, s).units) * a.hkv;
+    }
+    if (threadIdx.x == 0) a.unit0[a.seqs] = total;
+  }
+  if (count > 0 && before <= u0 && u0 < before + mine) {
+    int64_t at = before;
+    int s = s_beg;
+    for (;; ++s) {
+      const int64_t more = static_cast<int64_t>(seq_shape(a, s).units) * a.hkv;
+      if (u0 < at + more) break;
+      at += more;
+    }
+    sm.first_seq = s;
+    sm.skip = u0 - at;
+  }
+  return count;
+}
+
+}  // namespace
+}  // namespace stem
