@@ -623,17 +623,17 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
   for (int item = blockIdx.y; item < a.seqs * a.hkv; item += gridDim.y) {
     const int s = item / a.hkv, hk = item % a.hkv;
     const int64_t at = a.unit0[s];
-    const int64_t units = (a.unit0[s + 1] - at) / a.hkv;
-    if (units == 0) continue;
+    const int64_t len = div_floor(a.unit0[s + 1] - at, a.hkv);  // of an item
+    if (len == 0) continue;
     const int64_t total = a.unit0[a.seqs];
     const int used = ranges_used(a, total);
-    const int64_t first = at + hk * units, last = first + units - 1;
+    const int64_t begin = at + hk * len, first = begin + a.item_units, last = begin + len - 1;
     // the range that holds unit x: the largest k with range_begin(k) <= x
-    const int k0 = static_cast<int>(((first + 1) * used - 1) / total);
-    const int k1 = static_cast<int>(((last + 1) * used - 1) / total);
+    const int k0 = static_cast<int>(div_floor((first + 1) * used - 1, total));
+    const int k1 = static_cast<int>(div_floor((last + 1) * used - 1, total));
     if (k0 == k1) continue;  // not cut
     const SeqShape q = seq_shape(a, s);
-    const int slot0 = range_begin(total, used, k0) == first ? 0 : 1;
+    const int slot0 = range_begin(total, used, k0) >= begin ? 0 : 1;  // the first item of range k0, or a later one
     for (int r = blockIdx.x * rows_per_block; r < min((static_cast<int>(blockIdx.x) + 1) * rows_per_block, q.rows * a.group);
          ++r) {
       const int i = r / a.group, tile = i / a.tile_tokens;
@@ -695,8 +695,7 @@ static cudaError_t launch_tree_t(const TreeMaps& maps, const TreeArgs& args, cud
   if (e != cudaSuccess) return e;
   const int grid = args.ranges * args.tiles;
   if (args.unit_keys == kUnit) {
-    tree_attn_kernel<kFp8><<<grid, TreeCfg<kFp8>::kThreads, smem, stream>>>(maps, args);
-    e = cudaGetLastError();
+    e = launch_after(tree_attn_kernel<kFp8>, dim3(grid), TreeCfg<kFp8>::kThreads, smem, stream, maps, args);
   } else {
     e = launch_tree_narrow(maps, args, kFp8, stream);
   }
@@ -706,18 +705,9 @@ static cudaError_t launch_tree_t(const TreeMaps& maps, const TreeArgs& args, cud
   const int most = args.max_seq_tokens < args.total_tokens ? args.max_seq_tokens : args.total_tokens;
   const int64_t rows = static_cast<int64_t>(most) * args.group, items = static_cast<int64_t>(args.seqs) * args.hkv;
   // nothing is cut when one range holds everything: then only the status is left
-  cudaLaunchConfig_t cfg{};
-  const int64_t gx = args.ranges > 1 ? rows : 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(args.ranges > 1 ? (items < 65535 ? items : 65535) : 1));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, tree_join_kernel, j, grid, 1);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  const dim3 join(static_cast<unsigned>(args.ranges > 1 ? rows : 1),
+                  static_cast<unsigned>(args.ranges > 1 ? i64min(items, 65535) : 1));
+  return launch_after(tree_join_kernel, join, 128, 0, stream, j, grid, 1);
 }
 
 cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream) {

@@ -43,6 +43,7 @@ struct NarrowCfg {
   static constexpr int kSlabs = kFp8 ? 1 : 2;          // 128-byte slabs of a head row
   static constexpr int kUnitBytes = kUnit * kHeadDim * kElt;
   static constexpr int kTerms = kFp8 ? 3 : 2;          // columns per row of P^T
+  static constexpr int kStepKeys = kFp8 ? 32 : 16;     // keys per MMA of O^T
   static constexpr int kKSlots = kFp8 ? 6 : 3;
   static constexpr int kVSlots = kFp8 ? (kN == 16 ? 6 : 5) : (kN == 16 ? 3 : 2);
   static constexpr int kQBytes = kN * kHeadDim * kElt;
@@ -74,6 +75,12 @@ struct NarrowSmem {
   int status, abort;
   int odd_v[4];  // [item % 4]: item + 1 when a non-finite element of V was zeroed in it
 };
+
+// MMAs of O^T over unit u: those that hold a key before `kv` (one if none does).
+template <int kStepKeys>
+__device__ __forceinline__ int key_steps(int kv, int u) {
+  return max((min(kv - u * kUnit, kUnit) + kStepKeys - 1) / kStepKeys, 1);
+}
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -324,15 +331,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t sv = smem_u32(sm.v[slot]), sp = smem_u32(sm.p[h & 1]);
+          const int steps = key_steps<Cfg::kStepKeys>(wk.q.kv, u);
           if constexpr (kFp8) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 32 keys per step
-              mma_f8_ss(o_tmem, make_sdesc_sw128(sv + kk * 4096, kUnit * 128, 1024),
+              if (kk < steps) mma_f8_ss(o_tmem, make_sdesc_sw128(sv + kk * 4096, kUnit * 128, 1024),
                         make_sdesc_sw128(sp + kk * 32, 16, 1024), idesc_o, u != wk.ub || kk != 0);
           } else {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)  // 16 keys per step
-              mma_bf16_ss(o_tmem, make_sdesc_sw128(sv + kk * 2048, kUnit * 128, 1024),
+              if (kk < steps) mma_bf16_ss(o_tmem, make_sdesc_sw128(sv + kk * 2048, kUnit * 128, 1024),
                           make_sdesc_sw128(sp + (kk >> 2) * (Cfg::kTerms * kN * 128) + (kk & 3) * 32, 16, 1024), idesc_o,
                           u != wk.ub || kk != 0);
           }
@@ -362,14 +370,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = wk.q.rows * a.group;
       // per row: scale (e4m3: with the head's), reference less kBias, this key lane's share of the sum
       float c[kFp8 ? kN : 1], m[kN], l[kN];
+      float c_lane = a.scale_log2;  // row `lane`'s scale
       if constexpr (kFp8) {
-        const float mine = lane < rows ? a.scale_log2 * __ldg(a.q_scale + wk.hk_cur * a.group + lane % a.group) *
-                                             __ldg(a.k_scale + wk.hk_cur)
-                                       : 0.f;
+        if (lane < rows)
+          c_lane *= __ldg(a.q_scale + wk.hk_cur * a.group + lane % a.group) * __ldg(a.k_scale + wk.hk_cur);
 #pragma unroll
-        for (int r = 0; r < kN; ++r) c[r] = __shfl_sync(0xffffffffu, mine, r);
+        for (int r = 0; r < kN; ++r) c[r] = __shfl_sync(0xffffffffu, c_lane, r);
       } else {
-        c[0] = a.scale_log2;
+        c[0] = c_lane;
       }
 #pragma unroll
       for (int r = 0; r < kN; ++r) m[r] = l[r] = 0.f;
@@ -386,12 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = h % Cfg::kVSlots;
           good = good && mbar_wait(&sm.v_full[slot], (h / Cfg::kVSlots) & 1, abort, status);
           if (good) {
+            const int r0 = max(wk.q.ctx - u * kUnit, 0), r1 = Cfg::kStepKeys * key_steps<Cfg::kStepKeys>(wk.q.kv, u);
             bool odd = false;
 #pragma unroll 1
-            for (int x = kx; x < kUnit * 8 * Cfg::kSlabs; x += 128) {  // 16-byte chunk x: row (x / 8) % 128 of a slab
-              const int at_key = u * kUnit + ((x >> 3) & (kUnit - 1));
-              if (at_key < wk.q.ctx) continue;
-              uint4* at = reinterpret_cast<uint4*>(sm.v[slot] + x * 16);
+            for (int x = r0 * 8 * Cfg::kSlabs + kx; x < r1 * 8 * Cfg::kSlabs; x += 128) {
+              // 16-byte chunk x of rows r0 .. r1 - 1, slab by slab of a row
+              const int row = x / (8 * Cfg::kSlabs), chunk = x % (8 * Cfg::kSlabs);
+              const int at_key = u * kUnit + row;
+              uint4* at = reinterpret_cast<uint4*>(sm.v[slot] + (chunk >> 3) * (kUnit * 128) + row * 128 + (chunk & 7) * 16);
               uint4 w = *at;
               if (at_key >= wk.q.kv) w = make_uint4(0u, 0u, 0u, 0u);
               if constexpr (kFp8) {
@@ -420,26 +430,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < kN; x += 16) tmem_ld16(tmem + kN * b + lane_off + x, s + x);
         tmem_ld_wait();
-        if (edge && key >= wk.q.ctx) {
-          const int d = key - wk.q.ctx;  // index among the new tokens
-          int g = 0, i = 0;
-          bool see = false;
-#pragma unroll
-          for (int r = 0; r < kN; ++r) {
-            if (r < rows) {
-              if (g == 0)
-                see = key < wk.q.kv &&
-                      (a.mask == nullptr
-                           ? d <= i
-                           : (d >> 5) < a.mask_words &&
-                                 ((__ldg(a.mask + static_cast<size_t>(wk.q.tok0 + i) * a.mask_words + (d >> 5)) >> (d & 31)) & 1u));
-              if (!see) s[r] = 0xff800000u;  // -inf
-              if (++g == a.group) {
-                g = 0;
-                ++i;
-              }
+        uint32_t see = 0xffffffffu;  // rows that see this key
+        if (edge) {
+          if (key >= wk.q.ctx) {
+            const int d = key - wk.q.ctx;  // index among the new tokens
+            const uint32_t head_bits = 0xffffffffu >> (32 - a.group);
+            see = 0u;
+            if (key < wk.q.kv && (a.mask == nullptr || (d >> 5) < a.mask_words)) {
+              const uint32_t* word = a.mask + static_cast<size_t>(wk.q.tok0) * a.mask_words + (d >> 5);
+#pragma unroll 1
+              for (int i = 0; i < wk.q.rows; ++i, word += a.mask_words)
+                if (a.mask == nullptr ? d <= i : (__ldg(word) >> (d & 31)) & 1u) see |= head_bits << (i * a.group);
             }
           }
+#pragma unroll
+          for (int r = 0; r < kN; ++r)
+            if (!((see >> r) & 1u)) s[r] = 0xff800000u;  // -inf
         }
         // t = s c - m; does a row pass its reference by more than the slack?
         float t[kN], top = ninf;
@@ -463,13 +469,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-#pragma unroll
-          for (int r = 0; r < kN; ++r) {
-            if (r < rows) {
-              const float x = warp_max(__uint_as_float(s[r]) == ninf ? ninf : __uint_as_float(s[r]) * c[kFp8 ? r : 0]);
-              if (lane == 0) sm.red[warp][r] = x;
-            }
+          float peak = ninf;
+#pragma unroll 1
+          for (int r = 0; r < rows; ++r) {
+            uint32_t x;  // again from TMEM: registers cannot be indexed
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(tmem + kN * b + lane_off + r));
+            tmem_ld_wait();
+            const float cr = kFp8 ? __shfl_sync(0xffffffffu, c_lane, r) : c_lane;
+            const float y = warp_max((see >> r) & 1u ? __uint_as_float(x) * cr : ninf);
+            if (lane == r) peak = y;
           }
+          if (lane < rows) sm.red[warp][lane] = peak;
           vote_any(false);
           float alpha = 1.f;
           bool scale = false;
@@ -651,8 +661,7 @@ static cudaError_t launch_narrow_t(const TreeMaps& maps, const TreeArgs& args, c
   const cudaError_t e = cudaFuncSetAttribute(tree_narrow_kernel<kFp8, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  tree_narrow_kernel<kFp8, kN><<<args.ranges, kThreads, smem, stream>>>(maps, args);
-  return cudaGetLastError();
+  return launch_after(tree_narrow_kernel<kFp8, kN>, dim3(args.ranges), kThreads, smem, stream, maps, args);
 }
 
 cudaError_t launch_tree_narrow(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream) {

@@ -155,6 +155,8 @@ struct TreeArgs {
   int ranges;           // ranges of keys at most (the grid is ranges * tiles)
   int part_rows;        // rows of a partial result in the workspace
   int unit_keys;        // keys of a unit: 64, or 128 in the narrow kernel
+  int item_units;       // units that starting and finishing an item is worth
+  int min_range;        // shortest range, in units
   int page_size, num_pages, max_pages, mask_words;
   const int32_t *cu_seqlens, *kv_lens, *page_table;
   const uint32_t* mask;
@@ -166,13 +168,14 @@ struct TreeArgs {
   // workspace
   int* status;
   int* cta_status;      // [grid]
-  int64_t* unit0;       // [seqs + 1]: 64-key units (times KV heads) before each sequence
+  int64_t* unit0;       // [seqs + 1]: length (of all KV heads' items) before each sequence
   float2* part_ml;      // [grid][2][part_rows]: reference max and sum
   float* part_o;        // [grid][2][part_rows][128]
 };
 constexpr int kTreeRanges = 296;    // two CTAs on each of 148 SMs
 constexpr int kNarrowRanges = 148;  // one CTA per SM
 constexpr int kNarrowRows = 32;     // query rows (tokens * group) up to which the narrow kernel is used
+constexpr int kItemUnits = 2, kNarrowMinRange = 4, kTreeMinRange = 6;
 cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
 cudaError_t launch_tree_narrow(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
 

@@ -9,8 +9,6 @@
 namespace stem {
 namespace {
 
-constexpr int kMinRangeKeys = 256;  // keys below which a range is not cut further
-
 // Keys and queries of one sequence, as the call sees them.
 struct SeqShape {
   int tok0, n, rows;  // first packed token, new tokens, tokens that are computed
@@ -35,17 +33,28 @@ __device__ __forceinline__ SeqShape seq_shape(const TreeArgs& a, int s) {
   return r;
 }
 
-__device__ __forceinline__ int64_t range_begin(int64_t total, int ranges, int k) { return total * k / ranges; }
-// ranges in use: none is shorter than kMinRangeKeys
+// All items are laid end to end and cut into equal ranges.  An item's length is
+// its units and a.item_units more, in front of them, for what starting and
+// finishing an item costs; those are walked over.
+__device__ __forceinline__ int64_t seq_length(const TreeArgs& a, const SeqShape& q) {
+  return q.units == 0 ? 0 : static_cast<int64_t>(q.units + a.item_units) * a.hkv;
+}
+// Floor of x / y (0 <= x, 0 < y): most operands fit 32 bits, whose division is far shorter.
+__device__ __forceinline__ int64_t div_floor(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+__device__ __forceinline__ int64_t range_begin(int64_t total, int ranges, int k) { return div_floor(total * k, ranges); }
+// ranges in use: none is shorter than a.min_range
 __device__ __forceinline__ int ranges_used(const TreeArgs& a, int64_t total) {
-  return static_cast<int>(i64max(i64min(a.ranges, total * a.unit_keys / kMinRangeKeys), 1));
+  return static_cast<int>(i64max(i64min(a.ranges, div_floor(total, a.min_range)), 1));
 }
 
 // Walks the items (sequence, KV head) of a range; every role walks alike.
 struct Walk {
-  int s, hk, unit;  // next item and its first unit
-  int64_t left;     // units of the range from there on
-  int index;        // items seen so far
+  int s, hk, at;  // next item and the place in it
+  int64_t left;   // length of the range from there on
+  int index;      // items with a unit in the range so far
   SeqShape q;
   // current item
   int hk_cur, ub, ue;
@@ -57,8 +66,9 @@ struct Walk {
     q.units = 0;
     if (count > 0) {
       q = seq_shape(a, s);
-      hk = static_cast<int>(skip / q.units);
-      unit = static_cast<int>(skip % q.units);
+      const int len = q.units + a.item_units;
+      hk = static_cast<int>(div_floor(skip, len));
+      at = static_cast<int>(skip - static_cast<int64_t>(hk) * len);
     }
   }
   // the next item whose sequence has this tile; false at the end of the range
@@ -75,15 +85,18 @@ struct Walk {
         } while (q.units == 0);
       }
       hk_cur = hk;
-      ub = unit;
-      ue = static_cast<int>(i64min(q.units, unit + left));
+      const int len = q.units + a.item_units;
+      const int to = static_cast<int>(i64min(len, at + left));
+      ub = max(at - a.item_units, 0);
+      ue = to - a.item_units;
       whole = ub == 0 && ue == q.units;
-      left -= ue - ub;
-      unit = ue;
-      if (ue == q.units) {
-        unit = 0;
+      left -= to - at;
+      at = to;
+      if (to == len) {
+        at = 0;
         ++hk;
       }
+      if (ue <= ub) continue;  // the range ends before the item's first unit
       ++index;
       if (tile * a.tile_tokens < q.rows) return true;
     }
@@ -161,14 +174,10 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& odd) {
 }
 
 // Where a range starts, found by all threads of the CTA (kThreads of them):
-// prefix sums of the sequences' units.
-struct RangeStart {
-  int64_t skip, count;  // units of first_seq before the range; units of the range
-  int first_seq;
-};
+// prefix sums of the sequences' lengths.
 struct RangeScratch {
   int64_t scan[16];
-  int64_t skip;
+  int64_t skip;  // length of first_seq before the range
   int first_seq;
 };
 // One __syncthreads inside; the caller's next one publishes skip and first_seq
@@ -176,6 +185,8 @@ struct RangeScratch {
 // kernel and reports bad lengths.
 template <int kThreads>
 __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, RangeScratch& sm, int* status) {
+  // the first read of memory that earlier kernels may still be writing
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = warp_id(), lane = lane_id();
   const int per = (a.seqs + kThreads - 1) / kThreads;
   const int s_beg = min(static_cast<int>(threadIdx.x) * per, a.seqs), s_end = min(s_beg + per, a.seqs);
@@ -183,7 +194,7 @@ __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, Rang
   bool bad = false;
   for (int s = s_beg; s < s_end; ++s) {
     const SeqShape q = seq_shape(a, s);
-    mine += q.units;
+    mine += seq_length(a, q);
     bad |= q.bad;
   }
   int64_t incl = mine;
@@ -200,9 +211,6 @@ __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, Rang
     if (w < warp) before += sm.scan[w];
     total += sm.scan[w];
   }
-  before *= a.hkv;
-  mine *= a.hkv;
-  total *= a.hkv;
   const int used = ranges_used(a, total);
   const int64_t u0 = range < used ? range_begin(total, used, range) : total;
   const int64_t count = range < used ? range_begin(total, used, range + 1) - u0 : 0;
@@ -211,7 +219,7 @@ __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, Rang
     int64_t at = before;
     for (int s = s_beg; s < s_end; ++s) {
       a.unit0[s] = at;
-      at += static_cast<int64_t>(seq_shape(a, s).units) * a.hkv;
+      at += seq_length(a, seq_shape(a, s));
     }
     if (threadIdx.x == 0) a.unit0[a.seqs] = total;
   }
@@ -219,7 +227,7 @@ __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, Rang
     int64_t at = before;
     int s = s_beg;
     for (;; ++s) {
-      const int64_t more = static_cast<int64_t>(seq_shape(a, s).units) * a.hkv;
+      const int64_t more = seq_length(a, seq_shape(a, s));
       if (u0 < at + more) break;
       at += more;
     }
@@ -227,6 +235,23 @@ __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, Rang
     sm.skip = u0 - at;
   }
   return count;
+}
+
+// Launches a kernel whose start may overlap the end of the one before it in the
+// stream (it waits for that one in griddepcontrol.wait).
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
