@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
     __syncwarp();
   } else if (warp == kMmaIssuer) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc_s = make_idesc(kFp8 ? 0u : 1u, 0u, 128u, static_cast<uint32_t>(kUnit));
       const uint32_t idesc_o = make_idesc(kFp8 ? 0u : 1u, 1u, 128u, 128u);
       const uint32_t o_tmem = tmem + 128;
@@ -254,19 +254,19 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
         const int slot = hs % Cfg::kKSlots;
         if (!mbar_wait(&sm.k_full[slot], (hs / Cfg::kKSlots) & 1, abort, status)) return false;
         tc_fence_after();
-        const uint32_t sq = smem_u32(sm.q) + (qitem % qbufs) * Cfg::kSlabs * qslab;
-        const uint32_t sk = smem_u32(sm.k[slot]);
+        const uint64_t dq = make_sdesc_sw128(smem_u32(sm.q) + (qitem % qbufs) * Cfg::kSlabs * qslab, 16, 1024);
+        const uint64_t dk = make_sdesc_sw128(smem_u32(sm.k[slot]), 16, 1024);
         const uint32_t d = tmem + kUnit * (hs & 1);
+        // descriptors count 16-byte units
         if constexpr (kFp8) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f8_ss(d, make_sdesc_sw128(sq + kk * 32, 16, 1024), make_sdesc_sw128(sk + kk * 32, 16, 1024), idesc_s,
-                      kk != 0);
+            mma_f8_ss(d, dq + kk * 2, dk + kk * 2, idesc_s, kk != 0);
         } else {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ss(d, make_sdesc_sw128(sq + (kk >> 2) * qslab + (kk & 3) * 32, 16, 1024),
-                        make_sdesc_sw128(sk + (kk >> 2) * (kUnit * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk != 0);
+            mma_bf16_ss(d, dq + (kk >> 2) * (qslab >> 4) + (kk & 3) * 2, dk + (kk >> 2) * (kUnit * 8) + (kk & 3) * 2, idesc_s,
+                        kk != 0);
         }
         mma_commit(&sm.k_empty[slot]);
         mma_commit(&sm.s_full[hs & 1]);
@@ -289,16 +289,15 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
                mbar_wait(vbar, (kFp8 ? h >> 1 : h / Cfg::kVSlots) & 1, abort, status);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sv = smem_u32(kFp8 ? sm.wide[h & 1] : sm.v[slot]);
+          const uint64_t dv = make_sdesc_sw128(smem_u32(kFp8 ? sm.wide[h & 1] : sm.v[slot]), kUnit * 128, 1024);
           const uint32_t p = tmem + kUnit * (h & 1);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // 16 keys per step
-            mma_bf16_ts(o_tmem, p + kk * 8, make_sdesc_sw128(sv + kk * 2048, kUnit * 128, 1024), idesc_o,
-                        u != wk.ub || kk != 0);
+            mma_bf16_ts(o_tmem, p + kk * 8, dv + kk * 128, idesc_o, u != wk.ub || kk != 0);
           if constexpr (!kFp8) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // the low parts of P
-              mma_bf16_ts(o_tmem, p + 32 + kk * 8, make_sdesc_sw128(sv + kk * 2048, kUnit * 128, 1024), idesc_o, 1u);
+              mma_bf16_ts(o_tmem, p + 32 + kk * 8, dv + kk * 128, idesc_o, 1u);
             mma_commit(&sm.v_empty[slot]);
           }
           mma_commit(&sm.pv_done[h & 1]);
@@ -600,19 +599,24 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
   }
 }
 
-// Joins the pieces of the items that were cut: one block per (row, sequence x
-// KV head), its four warps take every fourth piece.  Block 0 also reduces the
-// CTAs' status.
-__global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas, int rows_per_block) {
-  __shared__ float sm_o[4][kHeadDim];
-  __shared__ float2 sm_ml[4];
+// Joins the pieces of the items that were cut.  blockIdx.y: item (sequence x KV
+// head), blockIdx.x: rows of it.  A warp takes a row; rows of many pieces are
+// taken by all warps of the block, every kJoinWarps-th piece each.  The order
+// of the sums is that of the ranges.  Block 0 also reduces the CTAs' status.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinAlone = 8;  // pieces up to which a warp takes a row alone
+
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas, int rows_per_block) {
+  __shared__ float sm_o[kJoinWarps][kHeadDim];
+  __shared__ float sm_l[kJoinWarps];
   __shared__ int sm_status;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = warp_id(), lane = lane_id();
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     if (threadIdx.x == 0) sm_status = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < ctas; i += 128) {
+    for (int i = threadIdx.x; i < ctas; i += kJoinWarps * 32) {
       const int st = a.cta_status[i];
       if (st != 0) atomicCAS(&sm_status, 0, st);
     }
@@ -620,13 +624,13 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
     if (threadIdx.x == 0) *a.status = sm_status;
   }
   const float ninf = -__int_as_float(0x7f800000);
+  const int64_t total = a.unit0[a.seqs];
+  const int used = ranges_used(a, total);
   for (int item = blockIdx.y; item < a.seqs * a.hkv; item += gridDim.y) {
     const int s = item / a.hkv, hk = item % a.hkv;
     const int64_t at = a.unit0[s];
     const int64_t len = div_floor(a.unit0[s + 1] - at, a.hkv);  // of an item
     if (len == 0) continue;
-    const int64_t total = a.unit0[a.seqs];
-    const int used = ranges_used(a, total);
     const int64_t begin = at + hk * len, first = begin + a.item_units, last = begin + len - 1;
     // the range that holds unit x: the largest k with range_begin(k) <= x
     const int k0 = static_cast<int>(div_floor((first + 1) * used - 1, total));
@@ -634,54 +638,79 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
     if (k0 == k1) continue;  // not cut
     const SeqShape q = seq_shape(a, s);
     const int slot0 = range_begin(total, used, k0) >= begin ? 0 : 1;  // the first item of range k0, or a later one
-    for (int r = blockIdx.x * rows_per_block; r < min((static_cast<int>(blockIdx.x) + 1) * rows_per_block, q.rows * a.group);
-         ++r) {
+    const bool together = k1 - k0 >= kJoinAlone;  // more pieces than that
+    const int rows = min((static_cast<int>(blockIdx.x) + 1) * rows_per_block, q.rows * a.group);
+    const float vscale = a.v_scale != nullptr ? __ldg(a.v_scale + hk) : 1.f;
+    for (int r = blockIdx.x * rows_per_block + (together ? 0 : warp); r < rows; r += together ? 1 : kJoinWarps) {
       const int i = r / a.group, tile = i / a.tile_tokens;
       const int row = r - tile * a.tile_tokens * a.group;
       auto part = [&](int k) -> size_t {
         return ((static_cast<size_t>(k) * a.tiles + tile) * 2 + (k == k0 ? slot0 : 0)) * a.part_rows + row;
       };
-      float m = ninf, l = 0.f;
+      float m = ninf, m_use, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      // the reference of the row: the largest of the pieces'
-      for (int k = k0 + lane; k <= k1; k += 32) m = fmaxf(m, a.part_ml[part(k)].x);
+      auto add = [&](float2 ml, float4 x) {
+        if (ml.x == ninf) return;  // the row sees no key of the piece
+        const float w = exp2f(ml.x - m_use);
+        l += w * ml.y;
+        o.x += w * x.x;
+        o.y += w * x.y;
+        o.z += w * x.z;
+        o.w += w * x.w;
+      };
+      if (!together) {
+        // every load of the row in flight at once
+        float2 ml[kJoinAlone];
+        float4 x[kJoinAlone];
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const float m_use = m == ninf ? 0.f : m;
-      for (int k = k0 + warp; k <= k1; k += 4) {
-        const size_t p = part(k);
-        const float2 ml = a.part_ml[p];
-        const float4 x = *reinterpret_cast<const float4*>(a.part_o + p * kHeadDim + lane * 4);
-        const float w = exp2f(ml.x - m_use);  // a piece without keys: exp2(-inf) = 0
-        if (ml.x != ninf) {
-          l += w * ml.y;
-          o.x += w * x.x;
-          o.y += w * x.y;
-          o.z += w * x.z;
-          o.w += w * x.w;
+        for (int j = 0; j < kJoinAlone; ++j) {
+          ml[j] = make_float2(ninf, 0.f);
+          if (k0 + j <= k1) {
+            const size_t p = part(k0 + j);
+            ml[j] = a.part_ml[p];
+            x[j] = *reinterpret_cast<const float4*>(a.part_o + p * kHeadDim + lane * 4);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinAlone; ++j) m = fmaxf(m, ml[j].x);
+        m_use = m == ninf ? 0.f : m;
+#pragma unroll
+        for (int j = 0; j < kJoinAlone; ++j) add(ml[j], x[j]);
+      } else {
+        for (int k = k0 + lane; k <= k1; k += 32) m = fmaxf(m, a.part_ml[part(k)].x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        m_use = m == ninf ? 0.f : m;
+#pragma unroll 4
+        for (int k = k0 + warp; k <= k1; k += kJoinWarps) {
+          const size_t p = part(k);
+          add(a.part_ml[p], *reinterpret_cast<const float4*>(a.part_o + p * kHeadDim + lane * 4));
         }
       }
-      *reinterpret_cast<float4*>(&sm_o[warp][lane * 4]) = o;
-      if (lane == 0) sm_ml[warp] = make_float2(m, l);
-      __syncthreads();
-      if (warp == 0) {
-        l = (sm_ml[0].y + sm_ml[1].y) + (sm_ml[2].y + sm_ml[3].y);
-        float acc[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[e] = (sm_o[0][lane * 4 + e] + sm_o[1][lane * 4 + e]) + (sm_o[2][lane * 4 + e] + sm_o[3][lane * 4 + e]);
-        float inv = l != 0.f ? 1.f / l : 0.f;
-        if (a.v_scale != nullptr) inv *= __ldg(a.v_scale + hk);
-        const int h = hk * a.group + r % a.group;
-        const size_t tok = static_cast<size_t>(q.tok0) + i;
-        uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) +
-                                              (tok * a.hq + h) * static_cast<size_t>(kHeadDim) * 2);
-        dst[lane] = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-        if (lane == 0)
-          a.lse[static_cast<size_t>(h) * a.total_tokens + tok] =
-              l != 0.f ? (m_use + log2f(l)) * 0.69314718055994530942f : ninf;
+      if (together) {
+        *reinterpret_cast<float4*>(&sm_o[warp][lane * 4]) = o;
+        if (lane == 0) sm_l[warp] = l;
+        __syncthreads();
+        if (warp == 0) {
+          for (int w = 1; w < kJoinWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(&sm_o[w][lane * 4]);
+            l += sm_l[w];
+            o.x += x.x;
+            o.y += x.y;
+            o.z += x.z;
+            o.w += x.w;
+          }
+        }
+        __syncthreads();
+        if (warp != 0) continue;
       }
-      __syncthreads();
+      const float inv = l != 0.f ? vscale / l : 0.f;
+      const int h = hk * a.group + r % a.group;
+      const size_t tok = static_cast<size_t>(q.tok0) + i;
+      reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + (tok * a.hq + h) * static_cast<size_t>(kHeadDim) * 2)[lane] =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (lane == 0)
+        a.lse[static_cast<size_t>(h) * a.total_tokens + tok] = l != 0.f ? (m_use + log2f(l)) * 0.69314718055994530942f : ninf;
     }
   }
 }
@@ -705,9 +734,12 @@ static cudaError_t launch_tree_t(const TreeMaps& maps, const TreeArgs& args, cud
   const int most = args.max_seq_tokens < args.total_tokens ? args.max_seq_tokens : args.total_tokens;
   const int64_t rows = static_cast<int64_t>(most) * args.group, items = static_cast<int64_t>(args.seqs) * args.hkv;
   // nothing is cut when one range holds everything: then only the status is left
-  const dim3 join(static_cast<unsigned>(args.ranges > 1 ? rows : 1),
+  // few rows in all: a block for each; else a row a warp, and more when the grid would exceed what runs at once
+  const int64_t blocks = (rows + kJoinWarps - 1) / kJoinWarps * items;
+  const int rows_per_block = rows * items <= 1024 ? 1 : kJoinWarps * static_cast<int>(i64min(blocks / 2048 + 1, 4));
+  const dim3 join(static_cast<unsigned>(args.ranges > 1 ? (rows + rows_per_block - 1) / rows_per_block : 1),
                   static_cast<unsigned>(args.ranges > 1 ? i64min(items, 65535) : 1));
-  return launch_after(tree_join_kernel, join, 128, 0, stream, j, grid, 1);
+  return launch_after(tree_join_kernel, join, kJoinWarps * 32, 0, stream, j, grid, rows_per_block);
 }
 
 cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream) {

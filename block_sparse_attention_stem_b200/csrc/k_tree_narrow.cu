@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kMmaIssuer) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t fmt = kFp8 ? 0u : 1u;  // e4m3 (kind::f8f6f4) or bf16 (kind::f16)
       const uint32_t idesc_s = make_idesc(fmt, 0u, 128u, static_cast<uint32_t>(kN));
       const uint32_t idesc_o = make_idesc(fmt, 0u, 128u, static_cast<uint32_t>(Cfg::kTerms * kN)) | (1u << 15);  // A MN-major
@@ -296,19 +296,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = hs % Cfg::kKSlots;
         if (!mbar_wait(&sm.k_full[slot], (hs / Cfg::kKSlots) & 1, abort, status)) return false;
         tc_fence_after();
-        const uint32_t sq = smem_u32(sm.q[qitem % kQBufs]);
-        const uint32_t sk = smem_u32(sm.k[slot]);
+        // descriptors count 16-byte units
+        const uint64_t dq = make_sdesc_sw128(smem_u32(sm.q[qitem % kQBufs]), 16, 1024);
+        const uint64_t dk = make_sdesc_sw128(smem_u32(sm.k[slot]), 16, 1024);
         const uint32_t d = tmem + kN * (hs & 1);
         if constexpr (kFp8) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // 32 dims per step
-            mma_f8_ss(d, make_sdesc_sw128(sk + kk * 32, 16, 1024), make_sdesc_sw128(sq + kk * 32, 16, 1024), idesc_s,
-                      kk != 0);
+            mma_f8_ss(d, dk + kk * 2, dq + kk * 2, idesc_s, kk != 0);
         } else {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // 16 dims per step
-            mma_bf16_ss(d, make_sdesc_sw128(sk + (kk >> 2) * (kUnit * 128) + (kk & 3) * 32, 16, 1024),
-                        make_sdesc_sw128(sq + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk != 0);
+            mma_bf16_ss(d, dk + (kk >> 2) * (kUnit * 8) + (kk & 3) * 2, dq + (kk >> 2) * (kN * 8) + (kk & 3) * 2, idesc_s,
+                        kk != 0);
         }
         mma_commit(&sm.k_empty[slot]);
         mma_commit(&sm.s_full[hs & 1]);
@@ -330,19 +330,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                mbar_wait(&sm.v_full[slot], (h / Cfg::kVSlots) & 1, abort, status);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sv = smem_u32(sm.v[slot]), sp = smem_u32(sm.p[h & 1]);
+          const uint64_t dv = make_sdesc_sw128(smem_u32(sm.v[slot]), kUnit * 128, 1024);
+          const uint64_t dp = make_sdesc_sw128(smem_u32(sm.p[h & 1]), 16, 1024);
           const int steps = key_steps<Cfg::kStepKeys>(wk.q.kv, u);
           if constexpr (kFp8) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 32 keys per step
-              if (kk < steps) mma_f8_ss(o_tmem, make_sdesc_sw128(sv + kk * 4096, kUnit * 128, 1024),
-                        make_sdesc_sw128(sp + kk * 32, 16, 1024), idesc_o, u != wk.ub || kk != 0);
+              if (kk < steps) mma_f8_ss(o_tmem, dv + kk * 256, dp + kk * 2, idesc_o, u != wk.ub || kk != 0);
           } else {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)  // 16 keys per step
-              if (kk < steps) mma_bf16_ss(o_tmem, make_sdesc_sw128(sv + kk * 2048, kUnit * 128, 1024),
-                          make_sdesc_sw128(sp + (kk >> 2) * (Cfg::kTerms * kN * 128) + (kk & 3) * 32, 16, 1024), idesc_o,
-                          u != wk.ub || kk != 0);
+              if (kk < steps)
+                mma_bf16_ss(o_tmem, dv + kk * 128, dp + (kk >> 2) * (Cfg::kTerms * kN * 8) + (kk & 3) * 2, idesc_o,
+                            u != wk.ub || kk != 0);
           }
           mma_commit(&sm.v_empty[slot]);
           mma_commit(&sm.pv_done[h & 1]);

@@ -175,7 +175,7 @@ struct TreeArgs {
 constexpr int kTreeRanges = 296;    // two CTAs on each of 148 SMs
 constexpr int kNarrowRanges = 148;  // one CTA per SM
 constexpr int kNarrowRows = 32;     // query rows (tokens * group) up to which the narrow kernel is used
-constexpr int kItemUnits = 2, kNarrowMinRange = 4, kTreeMinRange = 6;
+constexpr int kNarrowItemUnits = 2, kTreeItemUnits = 2, kNarrowMinRange = 4, kTreeMinRange = 6;
 cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
 cudaError_t launch_tree_narrow(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
 

@@ -282,7 +282,7 @@ stem_status_t stem_tree_attn(const stem_tree_t* tree, const stem_paged_kv_t* kv,
   a.ranges = l.ranges;
   a.part_rows = l.part_rows;
   a.unit_keys = l.unit_keys;
-  a.item_units = kItemUnits;
+  a.item_units = l.unit_keys == 128 ? kNarrowItemUnits : kTreeItemUnits;
   a.min_range = l.unit_keys == 128 ? kNarrowMinRange : kTreeMinRange;
   a.page_size = kv->page_size;
   a.num_pages = kv->num_pages;
