@@ -27,7 +27,7 @@
 // columns of S exactly), so its rounding does not add to the output's: with a
 // single bf16 P the error of a long average is as large as the output rounding
 // itself.  The second product is free while HBM is the bound.  e4m3: Q K^T on
-// the e4m3 operands, P in f16, V widened to f16 (exact) by two warps per unit.
+// the e4m3 operands, P in f16, V widened to f16 (exact) by warps of their own.
 //
 // Masked keys: S is replaced by -inf, so nothing in K matters.  A product 0 * v
 // would still carry a NaN or infinity of V into rows that do not see the key,
@@ -35,10 +35,10 @@
 // the end are zeroed in SMEM and non-finite elements of new tokens too; rows
 // that do see such an element get it added in the epilogue.
 //
-// 192 threads (256 for e4m3):
+// 192 threads (320 for e4m3):
 //   warps 0-3  softmax, epilogue (TMEM lane quarter = warp)
 //   warp  4    TMA producer of Q, K and V
-//   warp  5    TMEM owner and MMA issuer    warps 6-7 (e4m3)  V -> f16
+//   warp  5    TMEM owner and MMA issuer    warps 6-9 (e4m3)  V -> f16
 // Every wait is bounded; on expiry all roles leave and the call reports it.
 #include "stem_bsa_common.cuh"
 #include "stem_tree_common.cuh"
@@ -53,7 +53,9 @@ constexpr uint32_t kTmemCols = 256;  // S buffers at 0 and 64, O at 128
 
 template <bool kFp8>
 struct TreeCfg {
-  static constexpr int kThreads = kFp8 ? 256 : 192;
+  static constexpr int kWidenWarps = 4;
+  static constexpr bool kKeep = !kFp8;  // scores stay in registers between the maximum and the exponentials
+  static constexpr int kThreads = 192 + (kFp8 ? kWidenWarps * 32 : 0);
   static constexpr int kQBytes = kFp8 ? 16384 : 32768;
   static constexpr int kSlabs = kFp8 ? 1 : 2;  // 128-byte slabs of a head row
   static constexpr int kUnitBytes = kFp8 ? 8192 : 16384;
@@ -82,6 +84,13 @@ struct TreeSmem {
   int odd_v[4];  // [item % 4]: item + 1 when a non-finite element of V was zeroed in it
 };
 
+// Scores of keys that are not seen become -inf.
+__device__ __forceinline__ void hide(uint32_t (&rr)[32], uint32_t see) {
+#pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (!((see >> x) & 1u)) rr[x] = 0xff800000u;
+}
+
 }  // namespace
 
 template <bool kFp8>
@@ -106,7 +115,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.q_full[b], 1);
       mbar_init(&sm.q_empty[b], 1);
-      mbar_init(&sm.wide_full[b], 2);
+      mbar_init(&sm.wide_full[b], Cfg::kWidenWarps);
       mbar_init(&sm.s_full[b], 1);
       mbar_init(&sm.p_full[b], 4);
       mbar_init(&sm.pv_done[b], 1);
@@ -117,7 +126,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
     }
     for (int b = 0; b < Cfg::kVSlots; ++b) {
       mbar_init(&sm.v_full[b], 1);
-      mbar_init(&sm.v_empty[b], kFp8 ? 2 : 1);
+      mbar_init(&sm.v_empty[b], kFp8 ? Cfg::kWidenWarps : 1);
     }
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
@@ -293,11 +302,12 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           const uint32_t p = tmem + kUnit * (h & 1);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // 16 keys per step
-            mma_bf16_ts(o_tmem, p + kk * 8, dv + kk * 128, idesc_o, u != wk.ub || kk != 0);
+            mma_bf16_ts(o_tmem, p + (kFp8 ? kk * 8 : (kk >> 1) * 32 + (kk & 1) * 8), dv + kk * 128, idesc_o,
+                        u != wk.ub || kk != 0);
           if constexpr (!kFp8) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // the low parts of P
-              mma_bf16_ts(o_tmem, p + 32 + kk * 8, dv + kk * 128, idesc_o, 1u);
+              mma_bf16_ts(o_tmem, p + (kk >> 1) * 32 + (kk & 1) * 8 + 16, dv + kk * 128, idesc_o, 1u);
             mma_commit(&sm.v_empty[slot]);
           }
           mma_commit(&sm.pv_done[h & 1]);
@@ -327,10 +337,9 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           const bool check = (u + 1) * kUnit > wk.q.ctx;
           const int end = wk.q.kv - u * kUnit;  // rows from here on are behind the keys
           bool odd = false;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = (t >> 3) + 8 * i;
-            uint4 x = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
+#pragma unroll 1
+          for (int r = t >> 3; r < kUnit; r += Cfg::kWidenWarps * 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
             uint32_t w[8];
             const uint32_t in[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -425,34 +434,39 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           fence_async_smem();
         }
         if (active) {
-          uint32_t rr[2][32];
-          tmem_ld32(s_tmem, rr[0]);
-          tmem_ld32(s_tmem + 32, rr[1]);
-          tmem_ld_wait();
-          if (edge) {
-            const uint64_t see = valid ? visible(a, wk.q, i, u * kUnit) : 0ull;
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              const uint32_t bits = static_cast<uint32_t>(see >> (32 * ch));
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!((bits >> x) & 1u)) rr[ch][x] = 0xff800000u;  // -inf
-            }
+          const uint64_t see = !edge ? ~0ull : valid ? visible(a, wk.q, i, u * kUnit) : 0ull;
+          // 32 keys at a time.  bf16: the scores stay in registers.  e4m3: they are
+          // read again from TMEM, which keeps the code short enough for the
+          // instruction cache that all roles share, and the threads at 96 registers.
+          uint32_t rr[Cfg::kKeep ? 2 : 1][32];
+          float top = ninf;
+          if constexpr (Cfg::kKeep) {
+            tmem_ld32(s_tmem, rr[0]);
+            tmem_ld32(s_tmem + 32, rr[1]);
+            tmem_ld_wait();
           }
-          float m4[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            m4[e] = fmax3(__uint_as_float(rr[e >> 1][(e & 1) * 16]), __uint_as_float(rr[e >> 1][(e & 1) * 16 + 1]),
-                          __uint_as_float(rr[e >> 1][(e & 1) * 16 + 2]));
-#pragma unroll
-          for (int x = 3; x < 15; x += 2)
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t(&x32)[32] = rr[Cfg::kKeep ? ch : 0];
+            if constexpr (!Cfg::kKeep) {
+              tmem_ld32(s_tmem + 32 * ch, x32);
+              tmem_ld_wait();
+            }
+            if (edge) hide(x32, static_cast<uint32_t>(see >> (32 * ch)));
+            float m4[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              m4[e] = fmax3(m4[e], __uint_as_float(rr[e >> 1][(e & 1) * 16 + x]),
-                            __uint_as_float(rr[e >> 1][(e & 1) * 16 + x + 1]));
+              m4[e] = fmax3(__uint_as_float(x32[e * 8]), __uint_as_float(x32[e * 8 + 1]), __uint_as_float(x32[e * 8 + 2]));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(rr[e >> 1][(e & 1) * 16 + 15]));
-          const float m_cand = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c;
+            for (int x = 3; x < 7; x += 2)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                m4[e] = fmax3(m4[e], __uint_as_float(x32[e * 8 + x]), __uint_as_float(x32[e * 8 + x + 1]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(x32[e * 8 + 7]));
+            top = fmaxf(top, fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])));
+          }
+          const float m_cand = top == ninf ? ninf : top * c;
           const bool need =
               valid && ((m_ref == ninf) ? (m_cand != ninf) : (m_cand > m_ref + BsaCfg<kFp8>::kRescaleLog2));
           if (__any_sync(0xffffffffu, need)) {
@@ -482,13 +496,19 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           const float m_use = (m_ref == ninf) ? 0.f : m_ref;
           const float2 c2 = make_float2(c, c), nm2 = make_float2(-m_use, -m_use);
           float2 ps0 = make_float2(0.f, 0.f), ps1 = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll (Cfg::kKeep ? 2 : 1)
           for (int ch = 0; ch < 2; ++ch) {
             uint32_t hi[16], lo[16];
+            uint32_t(&x32)[32] = rr[Cfg::kKeep ? ch : 0];
+            if constexpr (!Cfg::kKeep) {
+              tmem_ld32(s_tmem + 32 * ch, x32);
+              tmem_ld_wait();
+              if (edge) hide(x32, static_cast<uint32_t>(see >> (32 * ch)));
+            }
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
-              const float2 e = ffma2(
-                  make_float2(__uint_as_float(rr[ch][2 * x]), __uint_as_float(rr[ch][2 * x + 1])), c2, nm2);
+              const float2 e =
+                  ffma2(make_float2(__uint_as_float(x32[2 * x]), __uint_as_float(x32[2 * x + 1])), c2, nm2);
               const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
               if (x & 1) ps1 = fadd2(ps1, p);
               else ps0 = fadd2(ps0, p);
@@ -505,8 +525,9 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
                 lo[x] = pack_bf16x2(r.x, r.y);
               }
             }
-            tmem_st16(s_tmem + 16 * ch, hi);
-            if constexpr (!kFp8) tmem_st16(s_tmem + 32 + 16 * ch, lo);
+            // P over the scores just read: bf16 in 32 columns (high, low parts), f16 in 16
+            tmem_st16(s_tmem + (kFp8 ? 16 : 32) * ch, hi);
+            if constexpr (!kFp8) tmem_st16(s_tmem + 32 * ch + 16, lo);
           }
           l += (ps0.x + ps0.y) + (ps1.x + ps1.y);
           tmem_st_wait();
@@ -527,7 +548,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
       const bool odd_v = *reinterpret_cast<volatile int*>(&sm.odd_v[item & 3]) == item + 1;
       if (active) {
         const size_t tok = static_cast<size_t>(wk.q.tok0) + i;
-        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + (wk.index > 1 ? 1 : 0)) * a.part_rows + row;
+        const size_t part = static_cast<size_t>(blockIdx.x) * 2 + (wk.index > 1 ? 1 : 0);
         float inv = (l != 0.f) ? 1.f / l : 0.f;
         if constexpr (kFp8) inv *= __ldg(a.v_scale + wk.hk_cur);
 #pragma unroll 1
@@ -571,9 +592,10 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
               dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * kHeadDim + ch * 32);
+            // dim by dim, so that a warp's 32 rows are one line
+            float* dst = a.part_o + (part * kHeadDim + ch * 32) * a.part_rows + row;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_uint4(rr[4 * q], rr[4 * q + 1], rr[4 * q + 2], rr[4 * q + 3]);
+            for (int x = 0; x < 32; ++x) dst[static_cast<size_t>(x) * a.part_rows] = __uint_as_float(rr[x]);
           }
         }
         if (valid) {
@@ -581,7 +603,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
             a.lse[static_cast<size_t>(hq) * a.total_tokens + tok] =
                 (l != 0.f) ? (m_ref + log2f(l)) * 0.69314718055994530942f : ninf;
           else
-            a.part_ml[part] = make_float2(m_ref, l);
+            a.part_ml[part * a.part_rows + row] = make_float2(m_ref, l);
         }
       }
       // the next item's first product into O waits for this warp's next P,
@@ -599,54 +621,68 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
   }
 }
 
-// Joins the pieces of the items that were cut.  blockIdx.y: item (sequence x KV
-// head), blockIdx.x: rows of it.  A warp takes a row; rows of many pieces are
-// taken by all warps of the block, every kJoinWarps-th piece each.  The order
-// of the sums is that of the ranges.  Block 0 also reduces the CTAs' status.
+// ---- joining the pieces of the items that were cut (blockIdx.y: item, that is
+// sequence x KV head), in the order of the ranges
+
+// The CTAs' status words become the call's.  One block.
+__device__ __forceinline__ void reduce_status(const TreeArgs& a, int ctas) {
+  __shared__ int sm_status;
+  if (threadIdx.x == 0) sm_status = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < ctas; i += blockDim.x) {
+    const int st = a.cta_status[i];
+    if (st != 0) atomicCAS(&sm_status, 0, st);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) *a.status = sm_status;
+}
+
+struct Pieces {
+  int s, hk;    // item
+  int k0, k1;   // ranges that hold a unit of it
+  int slot0;    // its slot in range k0: 0 when it is the first item there
+};
+// False when the item was not cut.
+__device__ __forceinline__ bool find_pieces(const TreeArgs& a, int item, Pieces* p) {
+  const int64_t total = a.unit0[a.seqs];
+  const int used = ranges_used(a, total);
+  p->s = item / a.hkv;
+  p->hk = item % a.hkv;
+  const int64_t at = a.unit0[p->s];
+  const int64_t len = div_floor(a.unit0[p->s + 1] - at, a.hkv);  // of an item
+  if (len == 0) return false;
+  const int64_t begin = at + p->hk * len, first = begin + a.item_units, last = begin + len - 1;
+  // the range that holds unit x: the largest k with range_begin(k) <= x
+  p->k0 = static_cast<int>(div_floor((first + 1) * used - 1, total));
+  p->k1 = static_cast<int>(div_floor((last + 1) * used - 1, total));
+  p->slot0 = range_begin(total, used, p->k0) >= begin ? 0 : 1;
+  return p->k0 != p->k1;
+}
+
+// Row-major pieces [rows][128] (narrow kernel).  A warp takes a row; rows of
+// many pieces are taken by all warps of the block, every kJoinWarps-th piece each.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinAlone = 8;  // pieces up to which a warp takes a row alone
 
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas, int rows_per_block) {
+    tree_join_rows_kernel(const __grid_constant__ TreeArgs a, int ctas, int rows_per_block) {
   __shared__ float sm_o[kJoinWarps][kHeadDim];
   __shared__ float sm_l[kJoinWarps];
-  __shared__ int sm_status;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = warp_id(), lane = lane_id();
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    if (threadIdx.x == 0) sm_status = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < ctas; i += kJoinWarps * 32) {
-      const int st = a.cta_status[i];
-      if (st != 0) atomicCAS(&sm_status, 0, st);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) *a.status = sm_status;
-  }
+  if (blockIdx.x == 0 && blockIdx.y == 0) reduce_status(a, ctas);
   const float ninf = -__int_as_float(0x7f800000);
-  const int64_t total = a.unit0[a.seqs];
-  const int used = ranges_used(a, total);
   for (int item = blockIdx.y; item < a.seqs * a.hkv; item += gridDim.y) {
-    const int s = item / a.hkv, hk = item % a.hkv;
-    const int64_t at = a.unit0[s];
-    const int64_t len = div_floor(a.unit0[s + 1] - at, a.hkv);  // of an item
-    if (len == 0) continue;
-    const int64_t begin = at + hk * len, first = begin + a.item_units, last = begin + len - 1;
-    // the range that holds unit x: the largest k with range_begin(k) <= x
-    const int k0 = static_cast<int>(div_floor((first + 1) * used - 1, total));
-    const int k1 = static_cast<int>(div_floor((last + 1) * used - 1, total));
-    if (k0 == k1) continue;  // not cut
-    const SeqShape q = seq_shape(a, s);
-    const int slot0 = range_begin(total, used, k0) >= begin ? 0 : 1;  // the first item of range k0, or a later one
+    Pieces pc;
+    if (!find_pieces(a, item, &pc)) continue;
+    const int k0 = pc.k0, k1 = pc.k1, hk = pc.hk;
+    const SeqShape q = seq_shape(a, pc.s);
     const bool together = k1 - k0 >= kJoinAlone;  // more pieces than that
     const int rows = min((static_cast<int>(blockIdx.x) + 1) * rows_per_block, q.rows * a.group);
     const float vscale = a.v_scale != nullptr ? __ldg(a.v_scale + hk) : 1.f;
     for (int r = blockIdx.x * rows_per_block + (together ? 0 : warp); r < rows; r += together ? 1 : kJoinWarps) {
-      const int i = r / a.group, tile = i / a.tile_tokens;
-      const int row = r - tile * a.tile_tokens * a.group;
-      auto part = [&](int k) -> size_t {
-        return ((static_cast<size_t>(k) * a.tiles + tile) * 2 + (k == k0 ? slot0 : 0)) * a.part_rows + row;
-      };
+      const int i = r / a.group;
+      auto part = [&](int k) -> size_t { return (static_cast<size_t>(k) * 2 + (k == k0 ? pc.slot0 : 0)) * a.part_rows + r; };
       float m = ninf, m_use, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       auto add = [&](float2 ml, float4 x) {
@@ -715,6 +751,69 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
 }
 
+// Dim-major pieces [128][rows] (wide kernel): a lane takes a row, a warp kCols
+// dims of 32 rows.  blockIdx.x: tile, 32-row group of it and dims of the block.
+template <int kCols>
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_dims_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = warp_id(), lane = lane_id();
+  if (blockIdx.x == 0 && blockIdx.y == 0) reduce_status(a, ctas);
+  const float ninf = -__int_as_float(0x7f800000);
+  constexpr int kParts = kHeadDim / (kCols * kJoinWarps);  // blocks that share the dims
+  const int d0 = (static_cast<int>(blockIdx.x) % kParts * kJoinWarps + warp) * kCols;
+  const int groups = a.part_rows / 32;
+  const int row = static_cast<int>(blockIdx.x) / kParts % groups * 32 + lane;
+  const int tile = static_cast<int>(blockIdx.x) / (kParts * groups);
+  const int ti = row / a.group, i = tile * a.tile_tokens + ti;
+  for (int item = blockIdx.y; item < a.seqs * a.hkv; item += gridDim.y) {
+    Pieces pc;
+    if (!find_pieces(a, item, &pc)) continue;
+    const SeqShape q = seq_shape(a, pc.s);
+    const bool valid = ti < a.tile_tokens && i < q.rows;
+    if (!__any_sync(0xffffffffu, valid)) continue;
+    auto part = [&](int k) -> size_t {
+      return (static_cast<size_t>(k) * a.tiles + tile) * 2 + (k == pc.k0 ? pc.slot0 : 0);
+    };
+    float m = ninf;
+#pragma unroll 4
+    for (int k = pc.k0; k <= pc.k1; ++k)
+      if (valid) m = fmaxf(m, a.part_ml[part(k) * a.part_rows + row].x);
+    const float m_use = m == ninf ? 0.f : m;
+    float l = 0.f, o[kCols];
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) o[e] = 0.f;
+#pragma unroll (32 / kCols)
+    for (int k = pc.k0; k <= pc.k1; ++k) {
+      if (valid) {
+        const size_t p = part(k);
+        const float2 ml = a.part_ml[p * a.part_rows + row];
+        const float* src = a.part_o + (p * kHeadDim + d0) * a.part_rows + row;
+        float x[kCols];
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) x[e] = src[static_cast<size_t>(e) * a.part_rows];
+        if (ml.x != ninf) {  // the piece holds a key that the row sees
+          const float w = exp2f(ml.x - m_use);
+          l += w * ml.y;
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) o[e] += w * x[e];
+        }
+      }
+    }
+    if (!valid) continue;
+    float inv = l != 0.f ? 1.f / l : 0.f;
+    if (a.v_scale != nullptr) inv *= __ldg(a.v_scale + pc.hk);
+    const int h = pc.hk * a.group + row % a.group;
+    const size_t tok = static_cast<size_t>(q.tok0) + i;
+    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) +
+                                          ((tok * a.hq + h) * static_cast<size_t>(kHeadDim) + d0) * 2);
+#pragma unroll
+    for (int e = 0; e < kCols; e += 4)
+      dst[e / 4] = make_uint2(pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv));
+    if (d0 == 0)
+      a.lse[static_cast<size_t>(h) * a.total_tokens + tok] = l != 0.f ? (m_use + log2f(l)) * 0.69314718055994530942f : ninf;
+  }
+}
+
 template <bool kFp8>
 static cudaError_t launch_tree_t(const TreeMaps& maps, const TreeArgs& args, cudaStream_t stream) {
   const size_t smem = sizeof(TreeSmem<kFp8>);
@@ -732,14 +831,22 @@ static cudaError_t launch_tree_t(const TreeMaps& maps, const TreeArgs& args, cud
   TreeArgs j = args;
   if (!kFp8) j.v_scale = nullptr;
   const int most = args.max_seq_tokens < args.total_tokens ? args.max_seq_tokens : args.total_tokens;
-  const int64_t rows = static_cast<int64_t>(most) * args.group, items = static_cast<int64_t>(args.seqs) * args.hkv;
-  // nothing is cut when one range holds everything: then only the status is left
-  // few rows in all: a block for each; else a row a warp, and more when the grid would exceed what runs at once
-  const int64_t blocks = (rows + kJoinWarps - 1) / kJoinWarps * items;
-  const int rows_per_block = rows * items <= 1024 ? 1 : kJoinWarps * static_cast<int>(i64min(blocks / 2048 + 1, 4));
-  const dim3 join(static_cast<unsigned>(args.ranges > 1 ? (rows + rows_per_block - 1) / rows_per_block : 1),
-                  static_cast<unsigned>(args.ranges > 1 ? i64min(items, 65535) : 1));
-  return launch_after(tree_join_kernel, join, kJoinWarps * 32, 0, stream, j, grid, rows_per_block);
+  const int64_t items = static_cast<int64_t>(args.seqs) * args.hkv;
+  const unsigned gy = static_cast<unsigned>(i64min(items, 65535));
+  if (args.ranges == 1)  // one range holds everything: nothing is cut, only the status is left
+    return launch_after(tree_join_rows_kernel, dim3(1), kJoinWarps * 32, 0, stream, j, grid, 0);
+  if (args.unit_keys == kUnit) {
+    // few items: more blocks, with fewer dims each
+    const int groups = args.tiles * (args.part_rows / 32);
+    if (groups * items >= 4 * 148)
+      return launch_after(tree_join_dims_kernel<16>, dim3(groups, gy), kJoinWarps * 32, 0, stream, j, grid);
+    return launch_after(tree_join_dims_kernel<4>, dim3(groups * 4, gy), kJoinWarps * 32, 0, stream, j, grid);
+  }
+  // few rows in all: a block for each; else a row a warp
+  const int rows = most * args.group;  // <= 32
+  const int rows_per_block = rows * items <= 1024 ? 1 : kJoinWarps;
+  return launch_after(tree_join_rows_kernel, dim3((rows + rows_per_block - 1) / rows_per_block, gy), kJoinWarps * 32, 0,
+                      stream, j, grid, rows_per_block);
 }
 
 cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream) {

@@ -121,13 +121,14 @@ stem_status_t tree_layout(const stem_tree_t* t, TreeLayout* out) {
   const bool narrow = most <= kNarrowRows / l.group;
   l.unit_keys = narrow ? 128 : 64;
   l.ranges = narrow ? kNarrowRanges : std::max(kTreeRanges / l.tiles, 1);
-  l.part_rows = l.ranges > 1 ? l.box_tokens * l.group : 0;  // one range: nothing is split
+  const int rows32 = (l.box_tokens * l.group + 31) / 32 * 32;
+  l.part_rows = narrow ? l.box_tokens * l.group : rows32;
   const size_t grid = std::max<size_t>(static_cast<size_t>(l.ranges) * l.tiles, kTreeRanges);
   l.off_cta = kStatusBytes;
   l.off_unit0 = l.off_cta + align256(grid * sizeof(int));
   l.off_ml = l.off_unit0 + align256((static_cast<size_t>(t->num_seqs) + 1) * sizeof(int64_t));
   // sized for the largest grid and tile of these heads, so that the size never shrinks with the lengths
-  const size_t parts = static_cast<size_t>(kTreeRanges) * 2 * l.box_tokens * l.group;
+  const size_t parts = static_cast<size_t>(kTreeRanges) * 2 * rows32;
   l.off_o = l.off_ml + align256(parts * sizeof(float2));
   l.bytes = l.off_o + align256(parts * kHeadDim * sizeof(float));
   *out = l;
