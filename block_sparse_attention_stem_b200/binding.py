@@ -27,6 +27,7 @@ STATUS_NAMES = {0: "STEM_OK", 1: "STEM_ERR_INVALID_ARG", 2: "STEM_ERR_UNSUPPORTE
                 6: "STEM_ERR_TIMEOUT", 7: "STEM_ERR_BAD_BLOCKLIST", 8: "STEM_ERR_BAD_INPUT",
                 9: "STEM_ERR_OUT_OF_PAGES"}
 STEM_BF16, STEM_FP8_E4M3 = 0, 1
+FP8_DTYPES = (torch.uint8, torch.float8_e4m3fn)
 EXPORTED = ("stem_plan", "stem_score", "stem_select", "stem_score_select", "stem_bsa_fwd", "stem_bsa_fwd_paged",
             "stem_prefill",
             "stem_prefill_host",
@@ -278,6 +279,14 @@ class PagedKV:
     page_table: torch.Tensor
     desc: StemPagedKV
 
+    def __post_init__(self):
+        # (device, e4m3, KV heads, head dim) of the pages; None when the two differ or are not contiguous
+        k, v = self.k_pages, self.v_pages
+        fp8 = k.dtype in FP8_DTYPES
+        same = (k.dtype == v.dtype and k.shape == v.shape and k.device == v.device == self.page_table.device
+                and k.dim() == 4 and k.is_contiguous() and v.is_contiguous() and (fp8 or k.dtype == torch.bfloat16))
+        self.kind = (k.device, fp8, k.shape[2], k.shape[3]) if same else None
+
 
 def paged_kv(k_pages, v_pages, page_table, page_size: int) -> PagedKV:
     """k_pages/v_pages [P, page_size, Hkv, d] device tensors, page_table int32
@@ -396,41 +405,36 @@ def stem_noalloc_read_device_status(stream=None) -> int:
 
 
 # ------------------------------------------------------------------ the paged cache
-def _on(device, stream):
+# These run once per layer and token: the checks are kept to a few comparisons
+# of attributes, and nothing is looked up that the descriptors already hold.
+def _on(device, stream) -> int:
     """The stream a call runs on: the caller's, or the current one of the tensors' device."""
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(device.index)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
-def _need(name, t, dtype, shape=None, device=None):
-    """A contiguous tensor of the documented type, shape (None: any extent) and device."""
-    kinds = dtype if isinstance(dtype, tuple) else (dtype,)
-    if t.dtype not in kinds or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {' or '.join(str(k) for k in kinds)} tensor, got {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
-        raise ValueError(f"{name} must have the shape {shape}, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
+def _run(device, stream, where, fn, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: the tensors must be on a GPU, not on {device}")
+    on = _on(device, stream)
+    if torch._C._cuda_getDevice() == device.index:
+        code = fn(*args, on)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, on)
+    if code != STEM_OK:
+        raise StemError(code, where)
 
 
-class _Device:
-    """Makes the tensors' device current for a call (a no-op when it is already)."""
-
-    def __init__(self, device):
-        self.index = device.index if device.type == "cuda" else None
-
-    def __enter__(self):
-        self.back = None
-        if self.index is not None and torch.cuda.current_device() != self.index:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _need(name, t, dtype, shape, device):
+    """A contiguous tensor of the documented type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 @dataclass
@@ -457,43 +461,44 @@ def stem_cache_extend(page_table, page_size: int, num_pages: int, cache_lens, ne
     workspace's status word."""
     dev = page_table.device
     i32 = torch.int32
-    _need("page_table", page_table, i32, (None, None))
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [num_seqs, max_pages]")
+    _need("page_table", page_table, i32, page_table.shape, dev)
     S = page_table.shape[0]
-    for name, t, shape in (("cache_lens", cache_lens, (S,)), ("new_lens", new_lens, (S,)),
-                           ("held_pages", held_pages, (S,)), ("free_pages", free_pages, (None,)),
-                           ("cursor", cursor, (1,))):
-        _need(name, t, i32, shape, dev)
+    per_seq = (S,)
+    _need("cache_lens", cache_lens, i32, per_seq, dev)
+    _need("new_lens", new_lens, i32, per_seq, dev)
+    _need("held_pages", held_pages, i32, per_seq, dev)
+    _need("free_pages", free_pages, i32, (free_pages.numel(),), dev)
+    _need("cursor", cursor, i32, (1,), dev)
     tree = parents is not None
     if tree:
         _need("parents", parents, i32, (max_tokens,), dev)
     words = mask_words if tree else 0
     if out is None:
-        # one allocation; each part starts on a 16-byte boundary
-        sizes = (S, 1, S + 1, S, max_tokens, max_tokens, max_tokens * words)
-        buf = torch.empty(sum((n + 3) & ~3 for n in sizes), dtype=i32, device=dev)
-        parts, at = [], 0
-        for n in sizes:
-            parts.append(buf[at:at + n])
-            at += (n + 3) & ~3
+        if max_tokens < 0 or words < 0:
+            raise ValueError("max_tokens and mask_words must not be negative")
+        sizes = (S, 1, S + 1, S, max_tokens, max_tokens, max_tokens * words)  # one allocation
+        parts = torch.empty(sum(sizes), dtype=i32, device=dev).split(sizes)
         out = CacheStep(*parts[:6], parts[6].view(max_tokens, words) if tree else None, None)
     else:
-        for name, t, shape in (("held", out.held, (S,)), ("cursor", out.cursor, (1,)),
-                               ("cu_seqlens", out.cu_seqlens, (S + 1,)), ("kv_lens", out.kv_lens, (S,)),
+        for name, t, shape in (("held", out.held, per_seq), ("cursor", out.cursor, (1,)),
+                               ("cu_seqlens", out.cu_seqlens, (S + 1,)), ("kv_lens", out.kv_lens, per_seq),
                                ("slots", out.slots, (max_tokens,)), ("positions", out.positions, (max_tokens,))):
             _need("out." + name, t, i32, shape, dev)
         if tree:
             if out.mask is None:
                 raise ValueError("out.mask is needed with parents")
             _need("out.mask", out.mask, i32, (max_tokens, words), dev)
-    out.ws = ws if ws is not None else out.ws if out.ws is not None else _ws(256, dev, None)
-    desc = StemCacheStep(S, max_tokens, page_size, num_pages, page_table.shape[1], free_pages.numel(), words,
-                         _ptr(cache_lens), _ptr(new_lens), _ptr(held_pages), _ptr(free_pages), _ptr(cursor),
-                         _ptr(parents))
-    with _Device(dev):
-        _check(LIB.stem_cache_extend(ctypes.byref(desc), _ptr(page_table), _ptr(out.held), _ptr(out.cursor),
-                                     _ptr(out.cu_seqlens), _ptr(out.kv_lens), _ptr(out.slots), _ptr(out.positions),
-                                     _ptr(out.mask) if tree else None, _ptr(out.ws), out.ws.numel(),
-                                     _on(dev, stream)), "stem_cache_extend")
+    if ws is None:
+        ws = out.ws if out.ws is not None else _ws(256, dev, None)
+    out.ws = ws
+    desc = StemCacheStep(S, max_tokens, page_size, num_pages, page_table.shape[1], free_pages.shape[0], words,
+                         cache_lens.data_ptr(), new_lens.data_ptr(), held_pages.data_ptr(), free_pages.data_ptr(),
+                         cursor.data_ptr(), parents.data_ptr() if tree else None)
+    _run(dev, stream, "stem_cache_extend", LIB.stem_cache_extend, ctypes.byref(desc), page_table.data_ptr(),
+         out.held.data_ptr(), out.cursor.data_ptr(), out.cu_seqlens.data_ptr(), out.kv_lens.data_ptr(),
+         out.slots.data_ptr(), out.positions.data_ptr(), out.mask.data_ptr() if tree else None, ws.data_ptr(), ws.numel())
     return out
 
 
@@ -509,14 +514,16 @@ def make_rope(rotary_dim=128, layout="half", base=1e6, scaling="plain", factor=1
 
 
 def _token_rows(name, t, T, device):
-    """Stride between the tokens of a bf16 [T, H, 128] tensor whose heads are contiguous."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T:
+    """(heads, stride between tokens) of a bf16 [T, H, d] tensor whose heads are contiguous."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[0] != T:
         raise ValueError(f"{name} must be a bf16 [{T}, H, d] tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    _, H, d = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != d):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if T > 1 else t.shape[1] * t.shape[2]
+    return H, st if T > 1 else H * d
 
 
 def stem_rope(rope: StemRope, q, k, v, positions, cache: PagedKV | None = None, slots=None, q_scale=None, k_scale=None,
@@ -527,44 +534,54 @@ def stem_rope(rope: StemRope, q, k, v, positions, cache: PagedKV | None = None, 
     None), k_out and v_out are made only without a cache.  Outputs are bf16, or
     e4m3 bytes (uint8) when the scales, fp32 [H], are given (or `fp8` says so).
     v may be None without a cache; so may q or k."""
-    T = positions.numel()
     dev = positions.device
-    _need("positions", positions, torch.int32, (T,))
+    T = positions.shape[0] if positions.dim() else 1
+    _need("positions", positions, torch.int32, (T,), dev)
     if fp8 is None:
         fp8 = q_scale is not None or k_scale is not None or v_scale is not None
-    kinds = (torch.uint8, torch.float8_e4m3fn) if fp8 else torch.bfloat16
-    heads = [0, 0, 0]
-    strides = [0, 0, 0]
-    for x, (name, t) in enumerate((("q", q), ("k", k), ("v", v))):
-        if t is not None:
-            strides[x], heads[x] = _token_rows(name, t, T, dev), t.shape[1]
-    if k is not None and v is not None and heads[1] != heads[2]:
+    hq = hk = hv = sq = sk = sv = 0
+    d = 128
+    if q is not None:
+        (hq, sq), d = _token_rows("q", q, T, dev), q.shape[2]
+    if k is not None:
+        (hk, sk), d = _token_rows("k", k, T, dev), k.shape[2]
+    if v is not None:
+        (hv, sv), d = _token_rows("v", v, T, dev), v.shape[2]
+    if k is not None and v is not None and hk != hv:
         raise ValueError("k and v must have the same heads")
-    hkv = heads[1] or heads[2]
-    d = next((t.shape[2] for t in (q, k, v) if t is not None), 128)
+    hkv = hk or hv
+    if any(t is not None and t.shape[2] != d for t in (q, k)):
+        raise ValueError("q, k and v must have the same head dimension")
     if cache is not None:
         if slots is None or k is None or v is None:
             raise ValueError("a cache needs k, v and slots")
         _need("slots", slots, torch.int32, (T,), dev)
-        for name, p in (("k_pages", cache.k_pages), ("v_pages", cache.v_pages)):
-            _need(name, p, kinds, (None, None, hkv, d), dev)
-    make = lambda h: torch.empty(T, h, d, dtype=torch.uint8 if fp8 else torch.bfloat16, device=dev)  # noqa: E731
-    if q_out is None and q is not None:
-        q_out = make(heads[0])
+        if cache.kind != (dev, fp8, hkv, d):
+            raise ValueError(f"the pages must be contiguous [P, page_size, {hkv}, {d}] on {dev} in "
+                             f"{'e4m3' if fp8 else 'bf16'}, got (device, e4m3, heads, dim) {cache.kind}")
+    made = torch.uint8 if fp8 else torch.bfloat16
+    if q_out is None:
+        if q is not None:
+            q_out = torch.empty((T, hq, d), dtype=made, device=dev)
+    else:
+        _need("q_out", q_out, q_out.dtype if fp8 and q_out.dtype in FP8_DTYPES else made, (T, hq, d), dev)
     if cache is None:
-        k_out = make(hkv) if k_out is None and k is not None else k_out
-        v_out = make(hkv) if v_out is None and v is not None else v_out
-    for name, t, h, sc in (("q", q_out, heads[0], q_scale), ("k", k_out, hkv, k_scale), ("v", v_out, hkv, v_scale)):
+        k_out = torch.empty((T, hkv, d), dtype=made, device=dev) if k_out is None and k is not None else k_out
+        v_out = torch.empty((T, hkv, d), dtype=made, device=dev) if v_out is None and v is not None else v_out
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
-            _need(name + "_out", t, kinds, (T, h, d), dev)
-        if sc is not None:
-            _need(name + "_scale", sc, torch.float32, (h,), dev)
-    io = StemRopeIO(T, heads[0], hkv, d, STEM_FP8_E4M3 if fp8 else STEM_BF16, _ptr(positions), _ptr(slots), _ptr(q),
-                    _ptr(k), _ptr(v), *strides, _ptr(q_scale), _ptr(k_scale), _ptr(v_scale), _ptr(q_out), _ptr(k_out),
+            _need(name, t, t.dtype if fp8 and t.dtype in FP8_DTYPES else made, (T, hkv, d), dev)
+    if fp8:
+        for name, t, h in (("q_scale", q_scale, hq), ("k_scale", k_scale, hkv), ("v_scale", v_scale, hkv)):
+            if t is not None:
+                _need(name, t, torch.float32, (h,), dev)
+    elif q_scale is not None or k_scale is not None or v_scale is not None:
+        raise ValueError("scales are for e4m3 outputs")
+    io = StemRopeIO(T, hq, hkv, d, STEM_FP8_E4M3 if fp8 else STEM_BF16, positions.data_ptr(), _ptr(slots), _ptr(q),
+                    _ptr(k), _ptr(v), sq, sk, sv, _ptr(q_scale), _ptr(k_scale), _ptr(v_scale), _ptr(q_out), _ptr(k_out),
                     _ptr(v_out))
-    with _Device(dev):
-        _check(LIB.stem_rope(ctypes.byref(rope), ctypes.byref(io), None if cache is None else ctypes.byref(cache.desc),
-                             _on(dev, stream)), "stem_rope")
+    _run(dev, stream, "stem_rope", LIB.stem_rope, ctypes.byref(rope), ctypes.byref(io),
+         None if cache is None else ctypes.byref(cache.desc))
     return q_out, k_out, v_out
 
 
@@ -589,13 +606,15 @@ def make_tree(q, cu_seqlens, kv_lens, num_kv_heads: int, mask=None, max_seq_toke
     max_seq_tokens (the most queries of one sequence) where it is known: with 0
     the launch is sized for T of them."""
     dev = q.device
-    fp8 = q.dtype in (torch.uint8, torch.float8_e4m3fn)
-    _need("q", q, (torch.bfloat16, torch.uint8, torch.float8_e4m3fn), (None, None, None))
+    fp8 = q.dtype in FP8_DTYPES
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    _need("q", q, q.dtype if fp8 else torch.bfloat16, q.shape, dev)
     S = kv_lens.numel()
     _need("kv_lens", kv_lens, torch.int32, (S,), dev)
     _need("cu_seqlens", cu_seqlens, torch.int32, (S + 1,), dev)
     if mask is not None:
-        _need("mask", mask, torch.int32, (q.shape[0], None), dev)
+        _need("mask", mask, torch.int32, (q.shape[0], mask.shape[-1]), dev)
     if fp8:
         for name, t, h in (("q_scale", q_scale, q.shape[1]), ("k_scale", k_scale, num_kv_heads),
                            ("v_scale", v_scale, num_kv_heads)):
@@ -620,25 +639,24 @@ def stem_tree_attn(tree: TreeQ, kv: PagedKV, out=None, lse=None, ws=None, stream
     q = tree.q
     dev = q.device
     T, hq, d = q.shape
-    fp8 = tree.desc.dtype == STEM_FP8_E4M3
-    kinds = (torch.uint8, torch.float8_e4m3fn) if fp8 else torch.bfloat16
-    for name, p in (("k_pages", kv.k_pages), ("v_pages", kv.v_pages)):
-        _need(name, p, kinds, (None, None, tree.desc.num_kv_heads, d), dev)
-    if kv.page_table.shape[0] < tree.desc.num_seqs or kv.page_table.device != dev:
-        raise ValueError("page_table must have a row per sequence, on the device of q")
+    desc = tree.desc
+    if kv.kind != (dev, desc.dtype == STEM_FP8_E4M3, desc.num_kv_heads, d):
+        raise ValueError(f"the pages must be contiguous [P, page_size, {desc.num_kv_heads}, {d}] on {dev} in "
+                         f"{'e4m3' if desc.dtype else 'bf16'}, got (device, e4m3, heads, dim) {kv.kind}")
+    if kv.page_table.shape[0] < desc.num_seqs:
+        raise ValueError("page_table must have a row per sequence")
     if out is None:
-        out = torch.empty(T, hq, d, dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
     else:
         _need("out", out, torch.bfloat16, (T, hq, d), dev)
     if lse is None:
-        lse = torch.empty(hq, T, dtype=torch.float32, device=dev)
+        lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
     else:
         _need("lse", lse, torch.float32, (hq, T), dev)
     if ws is None:
         ws = _ws(stem_tree_ws_bytes(tree), dev, None)
-    with _Device(dev):
-        _check(LIB.stem_tree_attn(ctypes.byref(tree.desc), ctypes.byref(kv.desc), _ptr(out), _ptr(lse), _ptr(ws),
-                                  ws.numel(), _on(dev, stream)), "stem_tree_attn")
+    _run(dev, stream, "stem_tree_attn", LIB.stem_tree_attn, ctypes.byref(desc), ctypes.byref(kv.desc), out.data_ptr(),
+         lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse, ws
 
 

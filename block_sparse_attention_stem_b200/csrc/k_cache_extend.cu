@@ -211,9 +211,11 @@ cudaError_t launch_cache_extend(const ExtendArgs& args, cudaStream_t stream) {
   unsigned ctas = 1;
   while (ctas < 8 && work > static_cast<int>(ctas) * kExtendThreads) ctas *= 2;
   const size_t smem = static_cast<size_t>(args.seqs) * 4 * sizeof(int32_t);
-  cudaError_t e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kMaxExtendSeqs * 4 * static_cast<int>(sizeof(int32_t)));
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kExtendThreads);

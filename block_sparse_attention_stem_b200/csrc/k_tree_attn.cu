@@ -818,8 +818,8 @@ template <bool kFp8>
 static cudaError_t launch_tree_t(const TreeMaps& maps, const TreeArgs& args, cudaStream_t stream) {
   const size_t smem = sizeof(TreeSmem<kFp8>);
   static_assert(sizeof(TreeSmem<kFp8>) <= 115712, "two CTAs per SM");
-  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(tree_attn_kernel<kFp8>), smem, allowed);
   if (e != cudaSuccess) return e;
   const int grid = args.ranges * args.tiles;
   if (args.unit_keys == kUnit) {

@@ -658,8 +658,8 @@ static cudaError_t launch_narrow_t(const TreeMaps& maps, const TreeArgs& args, c
   const size_t smem = sizeof(NarrowSmem<kFp8, kN>);
   static_assert(sizeof(NarrowSmem<kFp8, kN>) <= 232448, "227 KB per CTA");
   static_assert(sizeof(NarrowSmem<kFp8, kN>) > 116736, "one CTA per SM");
-  const cudaError_t e = cudaFuncSetAttribute(tree_narrow_kernel<kFp8, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(tree_narrow_kernel<kFp8, kN>), smem, allowed);
   if (e != cudaSuccess) return e;
   return launch_after(tree_narrow_kernel<kFp8, kN>, dim3(args.ranges), kThreads, smem, stream, maps, args);
 }

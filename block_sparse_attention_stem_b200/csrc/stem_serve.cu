@@ -38,7 +38,7 @@ stem_status_t check_pool(int32_t page_size, int32_t num_pages) {
 
 // Angular frequency of every rotated pair in units of 2^-64 turns per position.
 void rope_turns(const stem_rope_t& r, RopeArgs* a) {
-  const double two_pi = 6.283185307179586476925286766559;
+  constexpr long double kTwoPi = 6.283185307179586476925286766559005768L;
   const int half = r.rotary_dim / 2;
   double base = r.base;
   if (r.scaling == STEM_ROPE_NTK)
@@ -47,20 +47,23 @@ void rope_turns(const stem_rope_t& r, RopeArgs* a) {
   if (r.scaling == STEM_ROPE_YARN) {
     // the (fractional) pair that makes `turns` turns over the trained length
     auto pair_of = [&](double turns) {
-      return r.rotary_dim * std::log(r.original_len / (turns * two_pi)) / (2.0 * std::log(r.base));
+      return r.rotary_dim * std::log(r.original_len / (turns * static_cast<double>(kTwoPi))) / (2.0 * std::log(r.base));
     };
     low = std::max(std::floor(pair_of(r.beta_fast)), 0.0);
     high = std::min(std::ceil(pair_of(r.beta_slow)), r.rotary_dim - 1.0);
     if (low == high) high += 0.001;
   }
-  for (int j = 0; j < half; ++j) {
-    double w = std::pow(base, -2.0 * j / r.rotary_dim);
+  // w_j = ratio^j, carried in 64-bit mantissas: off by at most j 2^-63 of itself
+  const long double ratio = std::pow(static_cast<long double>(base), -2.0L / r.rotary_dim);
+  long double w_j = 1.0L;
+  for (int j = 0; j < half; ++j, w_j *= ratio) {
+    long double w = w_j;
     if (r.scaling == STEM_ROPE_LINEAR) w /= r.factor;
     if (r.scaling == STEM_ROPE_YARN) {
       const double t = std::min(std::max((j - low) / (high - low), 0.0), 1.0);
       w = w / r.factor * t + w * (1.0 - t);
     }
-    a->turn[j] = static_cast<uint64_t>(std::ldexp(w / two_pi, 64));  // w <= 1: below 2^62
+    a->turn[j] = static_cast<uint64_t>(w / kTwoPi * 18446744073709551616.0L);  // w <= 1: below 2^62
   }
   double amp = r.amplitude;
   if (amp == 0.0) amp = r.scaling == STEM_ROPE_YARN ? 0.1 * std::log(r.factor) + 1.0 : 1.0;
