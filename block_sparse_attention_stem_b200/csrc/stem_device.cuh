@@ -287,6 +287,15 @@ __device__ __forceinline__ float2 fsub2(float2 a, float2 b) {
   return *reinterpret_cast<float2*>(&d);
 }
 
+// Packed fp32 pair arithmetic (sm_100): d = a * b on both halves.
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
 // Packed fp32 pair arithmetic (sm_100): d = a * b + c on both halves.
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   uint64_t d;

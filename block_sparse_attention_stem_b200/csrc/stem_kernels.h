@@ -129,9 +129,8 @@ struct RopeArgs {
   float amplitude;
   int rotary_dim;
   int tokens;
-  int hq, hkv;                  // head rows of q and k to rotate (0: that tensor is not asked for)
+  int hq, hkv, hv;              // heads of q, k and v (0: that tensor is not asked for)
   int hkv_rows;                 // KV heads of a token
-  int has_v;
   const int32_t *positions, *slots;
   const uint8_t *q, *k, *v;     // bf16 rows
   int64_t q_stride, k_stride, v_stride;  // bytes between tokens

@@ -192,7 +192,7 @@ stem_status_t stem_rope(const stem_rope_t* rope, const stem_rope_io_t* io, const
   if (!io || io->num_tokens < 0 || io->num_q_heads < 0 || io->num_kv_heads < 0) return STEM_ERR_INVALID_ARG;
   if (io->out_dtype != STEM_BF16 && io->out_dtype != STEM_FP8_E4M3) return STEM_ERR_INVALID_ARG;
   if (io->head_dim != kHeadDim) return io->head_dim < 1 ? STEM_ERR_INVALID_ARG : STEM_ERR_UNSUPPORTED;
-  if (io->num_q_heads > 65536 || io->num_kv_heads > 65536) return STEM_ERR_INVALID_ARG;
+  if (io->num_q_heads > 4096 || io->num_kv_heads > 2048) return STEM_ERR_UNSUPPORTED;
   if (cache) {
     if ((st = check_pool(cache->page_size, cache->num_pages)) != STEM_OK) return st;
     if (!cache->k_pages || !cache->v_pages) return STEM_ERR_INVALID_ARG;
@@ -214,7 +214,7 @@ stem_status_t stem_rope(const stem_rope_t* rope, const stem_rope_io_t* io, const
   a.hq = io->q_out ? io->num_q_heads : 0;
   a.hkv = io->k_out || cache ? io->num_kv_heads : 0;
   a.hkv_rows = io->num_kv_heads;
-  a.has_v = io->v_out || cache;
+  a.hv = io->v_out || cache ? io->num_kv_heads : 0;
   a.positions = io->positions;
   a.slots = io->slots;
   a.q = static_cast<const uint8_t*>(io->q);

@@ -164,15 +164,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// d = a * b on both halves.
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
-
 // Non-finite bf16 elements (exponent 0xff) of a pair are zeroed.
 __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& odd) {
   if ((w & 0x7f80u) == 0x7f80u) {

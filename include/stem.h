@@ -427,8 +427,8 @@ typedef struct {
  * 16-byte aligned (positions, slots and scales 4-byte). */
 typedef struct {
   int32_t num_tokens;        /* T >= 0 */
-  int32_t num_q_heads;
-  int32_t num_kv_heads;
+  int32_t num_q_heads;       /* at most 4096 (STEM_ERR_UNSUPPORTED beyond) */
+  int32_t num_kv_heads;      /* at most 2048 */
   int32_t head_dim;          /* 128 */
   int32_t out_dtype;         /* stem_dtype_t of every output and of the pages */
   const int32_t* positions;  /* [T]; any int32 */
