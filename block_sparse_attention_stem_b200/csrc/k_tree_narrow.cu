@@ -1,17 +1,16 @@
 // k_tree_narrow.cu — attention over the paged cache for few query rows: single
-// tokens and small trees, at most 32 rows (tokens * query heads of a KV group)
-// per sequence and KV head.
+// tokens and the smallest trees, at most 16 rows (tokens * query heads of a KV
+// group) per sequence and KV head.
 //
 // The 128-row tile of the other kernel would be almost empty, and the tensor
 // cores would spend the same time and power on it.  Here the products are
 // turned round, so that the keys fill the 128 rows and the queries are the N
 // columns:
-//   S^T = K Q^T       128 keys x N rows, 8 steps (4 in e4m3)
+//   S^T = K Q^T       128 keys x 16 rows, 8 steps (4 in e4m3)
 //   P^T = exp2(..)    thread = key, one value per row, to SMEM as the B operand
-//   O^T += V^T P^T    128 dims x (N * terms), V^T read MN-major from the V tile
-// Both products read their A operand (K, V) once at SMEM speed: per 128 keys
-// about 0.5k tensor cycles where the wide kernel spends 1.7k, of the 2.8k
-// (bf16) that HBM takes to deliver them.
+//   O^T += V^T P^T    128 dims x (16 * terms), V^T read MN-major from the V tile
+// The tensor cores are 4% busy where the 128-row tile kept them at 50%, which
+// held the clock at 1.55 GHz under the power cap.
 //
 // Columns are cheap, so P is kept to more bits as several terms in columns of
 // their own, added in the epilogue.  bf16: two (cut off below p, and the rest).
@@ -22,9 +21,19 @@
 // key's share of every row's sum, and a value that passes the reference by more
 // than 2^kSlack is noticed by one barrier with a vote, which the four softmax
 // warps need anyway to agree on leaving.  Only then (always at an item's first
-// unit) are the rows' maxima reduced and O scaled.
+// unit) are the rows' maxima reduced and O scaled.  That code and the epilogue
+// are rolled loops: unrolled, an item switch in mid-stream waited 30 us for
+// instructions that the stream of keys had pushed out of L2 (which the keys'
+// evict-first policy prevents too).
 //
-// 192 threads, one CTA per SM (216 KB of SMEM, most of it K and V in flight):
+// Bound by HBM.  Measured: 16 tokens over 16K keys each (1.07 GB) 163 us, 6.59
+// TB/s; 64 over 1 to 8K 169 us; one over 128K (537 MB) 90 us.  Against 32 rows
+// the 128-row kernel is faster (eight tokens of four heads over 16K: 185 against
+// 211 us), since a thread's work grows with the rows.
+//
+// 192 threads; bf16: one CTA per SM (216 KB of SMEM, most of it K and V in
+// flight); e4m3: two, because a unit's chain of waits (about 1300 cycles) is as
+// long as HBM takes for its bytes:
 //   warps 0-3 softmax and epilogue, warp 4 TMA producer, warp 5 MMA issuer.
 #include "stem_tree_common.cuh"
 
@@ -35,36 +44,37 @@ namespace {
 constexpr int kUnit = 128;  // keys per tile
 constexpr int kThreads = 192;
 constexpr int kProducer = 4, kMmaIssuer = 5;
-constexpr int kQBufs = 4;
+constexpr int kN = 16;  // query rows at most
+constexpr int kQBufs = 2;
 
-template <bool kFp8, int kN>
+template <bool kFp8>
 struct NarrowCfg {
   static constexpr int kElt = kFp8 ? 1 : 2;
   static constexpr int kSlabs = kFp8 ? 1 : 2;          // 128-byte slabs of a head row
   static constexpr int kUnitBytes = kUnit * kHeadDim * kElt;
   static constexpr int kTerms = kFp8 ? 3 : 2;          // columns per row of P^T
   static constexpr int kStepKeys = kFp8 ? 32 : 16;     // keys per MMA of O^T
-  static constexpr int kKSlots = kFp8 ? 6 : 3;
-  static constexpr int kVSlots = kFp8 ? (kN == 16 ? 6 : 5) : (kN == 16 ? 3 : 2);
+  static constexpr int kSlots = 3;                     // of K, and of V
+  static constexpr int kCtas = kFp8 ? 2 : 1;           // per SM
   static constexpr int kQBytes = kN * kHeadDim * kElt;
   static constexpr int kPBytes = kTerms * kN * kUnit * kElt;
   static constexpr uint32_t kOCol = 2 * kN;            // S buffers at 0 and kN
-  static constexpr uint32_t kTmemCols = kN == 16 ? 128 : 256;
+  static constexpr uint32_t kTmemCols = 128;
   // P may reach 2^(kBias + kSlack): e4m3 ends at 448
   static constexpr float kBias = kFp8 ? 4.f : 0.f;
   static constexpr float kSlack = kFp8 ? 4.f : 8.f;
 };
 
-template <bool kFp8, int kN>
+template <bool kFp8>
 struct NarrowSmem {
-  using C = NarrowCfg<kFp8, kN>;
-  uint8_t k[C::kKSlots][C::kUnitBytes];  // 1024-aligned
-  uint8_t v[C::kVSlots][C::kUnitBytes];
+  using C = NarrowCfg<kFp8>;
+  uint8_t k[C::kSlots][C::kUnitBytes];  // 1024-aligned
+  uint8_t v[C::kSlots][C::kUnitBytes];
   uint8_t q[kQBufs][C::kQBytes];
   uint8_t p[2][C::kPBytes];
   uint64_t q_full[kQBufs], q_empty[kQBufs];
-  uint64_t k_full[C::kKSlots], k_empty[C::kKSlots];
-  uint64_t v_full[C::kVSlots], v_empty[C::kVSlots];
+  uint64_t k_full[C::kSlots], k_empty[C::kSlots];
+  uint64_t v_full[C::kSlots], v_empty[C::kSlots];
   uint64_t s_full[2];   // S^T_h complete
   uint64_t p_full[2];   // P^T_h stored (and O scaled)
   uint64_t pv_done[2];  // O += V^T_h P^T_h complete
@@ -124,12 +134,12 @@ __device__ __forceinline__ float2 from_e4m3x2(uint16_t v) {
 
 }  // namespace
 
-template <bool kFp8, int kN>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
     tree_narrow_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeArgs a) {
-  using Cfg = NarrowCfg<kFp8, kN>;
+  using Cfg = NarrowCfg<kFp8>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  NarrowSmem<kFp8, kN>& sm = *reinterpret_cast<NarrowSmem<kFp8, kN>*>(smem_raw);
+  NarrowSmem<kFp8>& sm = *reinterpret_cast<NarrowSmem<kFp8>*>(smem_raw);
   const int warp = warp_id(), lane = lane_id();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -142,11 +152,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.q_full[b], 1);
       mbar_init(&sm.q_empty[b], 1);
     }
-    for (int b = 0; b < Cfg::kKSlots; ++b) {
+    for (int b = 0; b < Cfg::kSlots; ++b) {
       mbar_init(&sm.k_full[b], 1);
       mbar_init(&sm.k_empty[b], 1);
     }
-    for (int b = 0; b < Cfg::kVSlots; ++b) {
+    for (int b = 0; b < Cfg::kSlots; ++b) {
       mbar_init(&sm.v_full[b], 1);
       mbar_init(&sm.v_empty[b], 1);
     }
@@ -184,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // units before V: while V_h is the next V, the products up to S_{h+1} can
     // complete, and the Q tile of K_{h+ahead-1} may have to wait for
     // S_{h+ahead-1-kQBufs} (items of one unit): ahead <= 2 + kQBufs.
-    constexpr int kAhead = Cfg::kKSlots < 2 + kQBufs ? Cfg::kKSlots : 2 + kQBufs;
+    constexpr int kAhead = Cfg::kSlots < 2 + kQBufs ? Cfg::kSlots : 2 + kQBufs;
     if (lane == 0) {
       tma_prefetch_desc(&maps.q);
       tma_prefetch_desc(&maps.k_pool);
@@ -248,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__shfl_sync(0xffffffffu, good, 0)) return false;
         ++item;
       }
-      if (!load(ks, &maps.k_pool, sm.k[0], sm.k_full, sm.k_empty, Cfg::kKSlots)) return false;
+      if (!load(ks, &maps.k_pool, sm.k[0], sm.k_full, sm.k_empty, Cfg::kSlots)) return false;
       if (ks.u == ks.w.ue) enter(ks);
       return true;
     };
@@ -258,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int x = 0; x < kAhead && ok && ks.more; ++x) ok = load_k();
     while (ok && vs.more) {
-      ok = load(vs, &maps.v_pool, sm.v[0], sm.v_full, sm.v_empty, Cfg::kVSlots);
+      ok = load(vs, &maps.v_pool, sm.v[0], sm.v_full, sm.v_empty, Cfg::kSlots);
       if (ok && vs.u == vs.w.ue) enter(vs);
       if (ok && ks.more) ok = load_k();
     }
@@ -271,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_quiesce(&full[x], (last / slots) & 1, status);
         }
       };
-      quiesce(sm.k_full, Cfg::kKSlots, ks.h);
-      quiesce(sm.v_full, Cfg::kVSlots, vs.h);
+      quiesce(sm.k_full, Cfg::kSlots, ks.h);
+      quiesce(sm.v_full, Cfg::kSlots, vs.h);
       quiesce(sm.q_full, kQBufs, item);
     }
     __syncwarp();
@@ -293,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++qitem;
           if (!mbar_wait(&sm.q_full[qitem % kQBufs], (qitem / kQBufs) & 1, abort, status)) return false;
         }
-        const int slot = hs % Cfg::kKSlots;
-        if (!mbar_wait(&sm.k_full[slot], (hs / Cfg::kKSlots) & 1, abort, status)) return false;
+        const int slot = hs % Cfg::kSlots;
+        if (!mbar_wait(&sm.k_full[slot], (hs / Cfg::kSlots) & 1, abort, status)) return false;
         tc_fence_after();
         // descriptors count 16-byte units
         const uint64_t dq = make_sdesc_sw128(smem_u32(sm.q[qitem % kQBufs]), 16, 1024);
@@ -325,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int h = 0;
       while (ok && wk.next(a, 0)) {
         for (int u = wk.ub; u < wk.ue && ok; ++u, ++h) {
-          const int slot = h % Cfg::kVSlots;
+          const int slot = h % Cfg::kSlots;
           ok = mbar_wait(&sm.p_full[h & 1], (h >> 1) & 1, abort, status) &&
-               mbar_wait(&sm.v_full[slot], (h / Cfg::kVSlots) & 1, abort, status);
+               mbar_wait(&sm.v_full[slot], (h / Cfg::kSlots) & 1, abort, status);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dv = make_sdesc_sw128(smem_u32(sm.v[slot]), kUnit * 128, 1024);
@@ -391,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key = u * kUnit + kx;
         if (edge) {
           // no NaN or infinity of V may meet a weight of zero
-          const int slot = h % Cfg::kVSlots;
-          good = good && mbar_wait(&sm.v_full[slot], (h / Cfg::kVSlots) & 1, abort, status);
+          const int slot = h % Cfg::kSlots;
+          good = good && mbar_wait(&sm.v_full[slot], (h / Cfg::kSlots) & 1, abort, status);
           if (good) {
             const int r0 = max(wk.q.ctx - u * kUnit, 0), r1 = Cfg::kStepKeys * key_steps<Cfg::kStepKeys>(wk.q.kv, u);
             bool odd = false;
@@ -653,21 +663,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kFp8, int kN>
+template <bool kFp8>
 static cudaError_t launch_narrow_t(const TreeMaps& maps, const TreeArgs& args, cudaStream_t stream) {
-  const size_t smem = sizeof(NarrowSmem<kFp8, kN>);
-  static_assert(sizeof(NarrowSmem<kFp8, kN>) <= 232448, "227 KB per CTA");
-  static_assert(sizeof(NarrowSmem<kFp8, kN>) > 116736, "one CTA per SM");
+  const size_t smem = sizeof(NarrowSmem<kFp8>);
+  static_assert(sizeof(NarrowSmem<kFp8>) <= (kFp8 ? 115712 : 232448), "CTAs per SM");
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(tree_narrow_kernel<kFp8, kN>), smem, allowed);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(tree_narrow_kernel<kFp8>), smem, allowed);
   if (e != cudaSuccess) return e;
-  return launch_after(tree_narrow_kernel<kFp8, kN>, dim3(args.ranges), kThreads, smem, stream, maps, args);
+  return launch_after(tree_narrow_kernel<kFp8>, dim3(args.ranges), kThreads, smem, stream, maps, args);
 }
 
 cudaError_t launch_tree_narrow(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream) {
-  if (args.box_rows <= 16)
-    return fp8 ? launch_narrow_t<true, 16>(maps, args, stream) : launch_narrow_t<false, 16>(maps, args, stream);
-  return fp8 ? launch_narrow_t<true, 32>(maps, args, stream) : launch_narrow_t<false, 32>(maps, args, stream);
+  return fp8 ? launch_narrow_t<true>(maps, args, stream) : launch_narrow_t<false>(maps, args, stream);
 }
 
 }  // namespace stem

@@ -172,8 +172,8 @@ struct TreeArgs {
   float* part_o;        // [grid][2]: [part_rows][128] (narrow kernel) or [128][part_rows]
 };
 constexpr int kTreeRanges = 296;    // two CTAs on each of 148 SMs
-constexpr int kNarrowRanges = 148;  // one CTA per SM
-constexpr int kNarrowRows = 32;     // query rows (tokens * group) up to which the narrow kernel is used
+constexpr int kNarrowRanges = 148;  // one CTA per SM (e4m3: twice as many, two per SM)
+constexpr int kNarrowRows = 16;     // query rows (tokens * group) up to which the narrow kernel is used
 constexpr int kNarrowItemUnits = 2, kTreeItemUnits = 5, kNarrowMinRange = 4, kTreeMinRange = 6;
 cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
 cudaError_t launch_tree_narrow(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);

@@ -123,7 +123,7 @@ stem_status_t tree_layout(const stem_tree_t* t, TreeLayout* out) {
   l.tiles = (most + l.tile_tokens - 1) / l.tile_tokens;
   const bool narrow = most <= kNarrowRows / l.group;
   l.unit_keys = narrow ? 128 : 64;
-  l.ranges = narrow ? kNarrowRanges : std::max(kTreeRanges / l.tiles, 1);
+  l.ranges = narrow ? kNarrowRanges * (t->dtype == STEM_FP8_E4M3 ? 2 : 1) : std::max(kTreeRanges / l.tiles, 1);
   const int rows32 = (l.box_tokens * l.group + 31) / 32 * 32;
   l.part_rows = narrow ? l.box_tokens * l.group : rows32;
   const size_t grid = std::max<size_t>(static_cast<size_t>(l.ranges) * l.tiles, kTreeRanges);
