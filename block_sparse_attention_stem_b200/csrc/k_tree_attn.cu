@@ -300,14 +300,15 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           tc_fence_after();
           const uint64_t dv = make_sdesc_sw128(smem_u32(kFp8 ? sm.wide[h & 1] : sm.v[slot]), kUnit * 128, 1024);
           const uint32_t p = tmem + kUnit * (h & 1);
+          const int steps = key_steps<kUnit, 16>(wk.q.kv, u);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // 16 keys per step
-            mma_bf16_ts(o_tmem, p + (kFp8 ? kk * 8 : (kk >> 1) * 32 + (kk & 1) * 8), dv + kk * 128, idesc_o,
+            if (kk < steps) mma_bf16_ts(o_tmem, p + (kFp8 ? kk * 8 : (kk >> 1) * 32 + (kk & 1) * 8), dv + kk * 128, idesc_o,
                         u != wk.ub || kk != 0);
           if constexpr (!kFp8) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // the low parts of P
-              mma_bf16_ts(o_tmem, p + (kk >> 1) * 32 + (kk & 1) * 8 + 16, dv + kk * 128, idesc_o, 1u);
+              if (kk < steps) mma_bf16_ts(o_tmem, p + (kk >> 1) * 32 + (kk & 1) * 8 + 16, dv + kk * 128, idesc_o, 1u);
             mma_commit(&sm.v_empty[slot]);
           }
           mma_commit(&sm.pv_done[h & 1]);
@@ -397,6 +398,14 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
       float c = a.scale_log2;
       if constexpr (kFp8) c *= __ldg(a.q_scale + hq) * __ldg(a.k_scale + wk.hk_cur);
       float m_ref = ninf, l = 0.f;
+      // the row's first mask words now, so that the item's last units do not wait for them
+      uint64_t known = 0ull;
+      const int words = a.mask == nullptr || !valid ? 0 : min(a.mask_words, 2);
+      if (words > 0) {
+        const uint32_t* row_words = a.mask + (static_cast<size_t>(wk.q.tok0) + i) * a.mask_words;
+        known = __ldg(row_words);
+        if (words > 1) known |= static_cast<uint64_t>(__ldg(row_words + 1)) << 32;
+      }
 #pragma unroll 1
       for (int u = wk.ub; u < wk.ue; ++u, ++h) {
         const int b = h & 1;
@@ -414,16 +423,14 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
             ok = false;
             break;
           }
-          const int end = wk.q.kv - u * kUnit;
+          const int r0 = max(wk.q.ctx - u * kUnit, 0), r1 = 16 * key_steps<kUnit, 16>(wk.q.kv, u);
           bool odd = false;
 #pragma unroll 1
-          for (int x = row; x < 2 * kUnit * 8; x += 128) {
-            const int r = (x >> 3) & (kUnit - 1);  // 16-byte chunk x of the two slabs: row r
-            const int key = u * kUnit + r;
-            if (key < wk.q.ctx) continue;
-            uint4* at = reinterpret_cast<uint4*>(sm.v[slot] + x * 16);
+          for (int x = r0 * 16 + row; x < r1 * 16; x += 128) {  // 16-byte chunk x % 16 of row x / 16
+            const int r = x >> 4;
+            uint4* at = reinterpret_cast<uint4*>(sm.v[slot] + ((x >> 3) & 1) * (kUnit * 128) + r * 128 + (x & 7) * 16);
             uint4 w = *at;
-            if (r >= end) w = make_uint4(0u, 0u, 0u, 0u);
+            if (u * kUnit + r >= wk.q.kv) w = make_uint4(0u, 0u, 0u, 0u);
             w.x = finite_bf16x2(w.x, odd);
             w.y = finite_bf16x2(w.y, odd);
             w.z = finite_bf16x2(w.z, odd);
@@ -434,7 +441,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           fence_async_smem();
         }
         if (active) {
-          const uint64_t see = !edge ? ~0ull : valid ? visible(a, wk.q, i, u * kUnit) : 0ull;
+          const uint64_t see = !edge ? ~0ull : valid ? visible(a, wk.q, i, u * kUnit, known, words) : 0ull;
           // 32 keys at a time.  bf16: the scores stay in registers.  e4m3: they are
           // read again from TMEM, which keeps the code short enough for the
           // instruction cache that all roles share, and the threads at 96 registers.
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           if (odd_v && valid) {
             // add the non-finite elements of V that this row does see
             for (int u = max(wk.ub, wk.q.ctx / kUnit); u < wk.ue; ++u) {
-              uint64_t see = visible(a, wk.q, i, u * kUnit);
+              uint64_t see = visible(a, wk.q, i, u * kUnit, known, words);
               for (; see != 0ull; see &= see - 1) {
                 const int key = u * kUnit + __ffsll(static_cast<long long>(see)) - 1;
                 if (key < wk.q.ctx) continue;
@@ -580,8 +587,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           }
           if (!valid) continue;
           if (wk.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) +
-                                                  (tok * a.hq + hq) * static_cast<size_t>(kHeadDim) * 2) + ch * 4;
+            uint8_t* dst = static_cast<uint8_t*>(a.out) + ((tok * a.hq + hq) * static_cast<size_t>(kHeadDim) + ch * 32) * 2;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t w[4];
@@ -589,7 +595,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
               for (int e = 0; e < 4; ++e)
                 w[e] = pack_bf16x2(__uint_as_float(rr[q * 8 + 2 * e]) * inv,
                                    __uint_as_float(rr[q * 8 + 2 * e + 1]) * inv);
-              dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(dst)[q] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
             // dim by dim, so that a warp's 32 rows are one line
@@ -755,6 +761,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 // dims of 32 rows.  blockIdx.x: tile, 32-row group of it and dims of the block.
 template <int kCols>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_dims_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+  __shared__ float sm_w[kTreeRanges][32], sm_m[kJoinWarps][32], sm_l[kJoinWarps][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = warp_id(), lane = lane_id();
   if (blockIdx.x == 0 && blockIdx.y == 0) reduce_status(a, ctas);
@@ -774,31 +781,48 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_dims_kernel(const _
     auto part = [&](int k) -> size_t {
       return (static_cast<size_t>(k) * a.tiles + tile) * 2 + (k == pc.k0 ? pc.slot0 : 0);
     };
+    // each warp takes every kJoinWarps-th piece's reference and sum; the weights go to SMEM
+    const int n = pc.k1 - pc.k0 + 1;
     float m = ninf;
 #pragma unroll 4
-    for (int k = pc.k0; k <= pc.k1; ++k)
-      if (valid) m = fmaxf(m, a.part_ml[part(k) * a.part_rows + row].x);
+    for (int k = warp; k < n; k += kJoinWarps)
+      if (valid) m = fmaxf(m, a.part_ml[part(pc.k0 + k) * a.part_rows + row].x);
+    sm_m[warp][lane] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sm_m[w][lane]);
     const float m_use = m == ninf ? 0.f : m;
-    float l = 0.f, o[kCols];
+    float l = 0.f;
+#pragma unroll 4
+    for (int k = warp; k < n; k += kJoinWarps) {
+      if (valid) {
+        const float2 ml = a.part_ml[part(pc.k0 + k) * a.part_rows + row];
+        const float w = exp2f(ml.x - m_use);  // 0 for a piece without a key that the row sees
+        sm_w[k][lane] = w;
+        l += w * ml.y;
+      }
+    }
+    sm_l[warp][lane] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) l += sm_l[w][lane];
+    float o[kCols];
 #pragma unroll
     for (int e = 0; e < kCols; ++e) o[e] = 0.f;
 #pragma unroll (32 / kCols)
-    for (int k = pc.k0; k <= pc.k1; ++k) {
+    for (int k = 0; k < n; ++k) {
       if (valid) {
-        const size_t p = part(k);
-        const float2 ml = a.part_ml[p * a.part_rows + row];
-        const float* src = a.part_o + (p * kHeadDim + d0) * a.part_rows + row;
-        float x[kCols];
+        const float* src = a.part_o + (part(pc.k0 + k) * kHeadDim + d0) * a.part_rows + row;
+        const float w = sm_w[k][lane];
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) x[e] = src[static_cast<size_t>(e) * a.part_rows];
-        if (ml.x != ninf) {  // the piece holds a key that the row sees
-          const float w = exp2f(ml.x - m_use);
-          l += w * ml.y;
-#pragma unroll
-          for (int e = 0; e < kCols; ++e) o[e] += w * x[e];
+        for (int e = 0; e < kCols; ++e) {
+          const float x = src[static_cast<size_t>(e) * a.part_rows];
+          if (w != 0.f) o[e] += w * x;  // (a piece of weight 0 may hold anything)
         }
       }
     }
+    __syncthreads();  // the next item writes the tables again
     if (!valid) continue;
     float inv = l != 0.f ? 1.f / l : 0.f;
     if (a.v_scale != nullptr) inv *= __ldg(a.v_scale + pc.hk);

@@ -86,12 +86,6 @@ struct NarrowSmem {
   int odd_v[4];  // [item % 4]: item + 1 when a non-finite element of V was zeroed in it
 };
 
-// MMAs of O^T over unit u: those that hold a key before `kv` (one if none does).
-template <int kStepKeys>
-__device__ __forceinline__ int key_steps(int kv, int u) {
-  return max((min(kv - u * kUnit, kUnit) + kStepKeys - 1) / kStepKeys, 1);
-}
-
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -342,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
           tc_fence_after();
           const uint64_t dv = make_sdesc_sw128(smem_u32(sm.v[slot]), kUnit * 128, 1024);
           const uint64_t dp = make_sdesc_sw128(smem_u32(sm.p[h & 1]), 16, 1024);
-          const int steps = key_steps<Cfg::kStepKeys>(wk.q.kv, u);
+          const int steps = key_steps<kUnit, Cfg::kStepKeys>(wk.q.kv, u);
           if constexpr (kFp8) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 32 keys per step
@@ -404,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
           const int slot = h % Cfg::kSlots;
           good = good && mbar_wait(&sm.v_full[slot], (h / Cfg::kSlots) & 1, abort, status);
           if (good) {
-            const int r0 = max(wk.q.ctx - u * kUnit, 0), r1 = Cfg::kStepKeys * key_steps<Cfg::kStepKeys>(wk.q.kv, u);
+            const int r0 = max(wk.q.ctx - u * kUnit, 0), r1 = Cfg::kStepKeys * key_steps<kUnit, Cfg::kStepKeys>(wk.q.kv, u);
             bool odd = false;
 #pragma unroll 1
             for (int x = r0 * 8 * Cfg::kSlabs + kx; x < r1 * 8 * Cfg::kSlabs; x += 128) {
@@ -616,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
           // add the non-finite elements of V that this row does see
 #pragma unroll 1
           for (int key = max(wk.ub * kUnit, wk.q.ctx); key < min(wk.ue * kUnit, wk.q.kv); ++key) {
-            if (!(visible(a, wk.q, i, key) & 1ull)) continue;
+            if (!(visible(a, wk.q, i, key, 0ull, 0) & 1ull)) continue;
             const int pr = pool_row(a, wk.s, key);
             if (pr >= a.num_pages * a.page_size) continue;
             const size_t at = (static_cast<size_t>(pr) * a.hkv + wk.hk_cur) * kHeadDim + kx;

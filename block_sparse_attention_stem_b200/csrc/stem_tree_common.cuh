@@ -106,8 +106,16 @@ struct Walk {
   }
 };
 
-// Bits of the 64 keys from `key0` on that query i of the sequence sees.
-__device__ __forceinline__ uint64_t visible(const TreeArgs& a, const SeqShape& q, int i, int key0) {
+// Steps of P V over unit u: those that hold a key before `kv` (one if none does).
+template <int kUnit, int kStepKeys>
+__device__ __forceinline__ int key_steps(int kv, int u) {
+  return max((min(kv - u * kUnit, kUnit) + kStepKeys - 1) / kStepKeys, 1);
+}
+
+// Bits of the 64 keys from `key0` on that query i of the sequence sees.  `known`
+// holds the first `words` (at most two) words of the query's mask row.
+__device__ __forceinline__ uint64_t visible(const TreeArgs& a, const SeqShape& q, int i, int key0, uint64_t known,
+                                            int words) {
   const int d0 = key0 - q.ctx;  // index, among the new tokens, of the first key
   uint64_t bits;
   if (a.mask == nullptr) {
@@ -117,7 +125,10 @@ __device__ __forceinline__ uint64_t visible(const TreeArgs& a, const SeqShape& q
     const uint32_t* row = a.mask + static_cast<size_t>(q.tok0 + i) * a.mask_words;
     const int from = max(d0, 0);
     const int w = from >> 5, sh = from & 31;
-    auto word = [&](int x) -> uint64_t { return x < a.mask_words ? __ldg(row + x) : 0u; };
+    auto word = [&](int x) -> uint64_t {
+      if (x < words) return x == 0 ? static_cast<uint32_t>(known) : static_cast<uint32_t>(known >> 32);
+      return x < a.mask_words ? __ldg(row + x) : 0u;
+    };
     const uint64_t lo = word(w) | word(w + 1) << 32;
     bits = sh == 0 ? lo : lo >> sh | word(w + 2) << (64 - sh);
     if (q.n - from < 64) bits &= (1ull << (q.n - from > 0 ? q.n - from : 0)) - 1;
