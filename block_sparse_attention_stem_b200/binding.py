@@ -479,7 +479,7 @@ def stem_cache_extend(page_table, page_size: int, num_pages: int, cache_lens, ne
         if max_tokens < 0 or words < 0:
             raise ValueError("max_tokens and mask_words must not be negative")
         sizes = (S, 1, S + 1, S, max_tokens, max_tokens, max_tokens * words)  # one allocation
-        parts = torch.empty(sum(sizes), dtype=i32, device=dev).split(sizes)
+        parts = torch.empty(sum(sizes), dtype=i32, device=dev).split_with_sizes(sizes)
         out = CacheStep(*parts[:6], parts[6].view(max_tokens, words) if tree else None, None)
     else:
         for name, t, shape in (("held", out.held, per_seq), ("cursor", out.cursor, (1,)),
@@ -514,16 +514,16 @@ def make_rope(rotary_dim=128, layout="half", base=1e6, scaling="plain", factor=1
 
 
 def _token_rows(name, t, T, device):
-    """(heads, stride between tokens) of a bf16 [T, H, d] tensor whose heads are contiguous."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[0] != T:
+    """(heads, head dim, stride between tokens) of a bf16 [T, H, d] tensor whose heads are contiguous."""
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[0] != T:
         raise ValueError(f"{name} must be a bf16 [{T}, H, d] tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
-    _, H, d = t.shape
-    st, sh, sd = t.stride()
-    if sd != 1 or (H > 1 and sh != d):
+    _, H, d = shape
+    if strides[2] != 1 or (H > 1 and strides[1] != d):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return H, st if T > 1 else H * d
+    return H, d, strides[0] if T > 1 else H * d
 
 
 def stem_rope(rope: StemRope, q, k, v, positions, cache: PagedKV | None = None, slots=None, q_scale=None, k_scale=None,
@@ -539,49 +539,68 @@ def stem_rope(rope: StemRope, q, k, v, positions, cache: PagedKV | None = None, 
     _need("positions", positions, torch.int32, (T,), dev)
     if fp8 is None:
         fp8 = q_scale is not None or k_scale is not None or v_scale is not None
-    hq = hk = hv = sq = sk = sv = 0
-    d = 128
+    hq = hkv = sq = sk = sv = 0
+    d = None
+    pq = pk = pv = pqo = pko = pvo = pslots = None
     if q is not None:
-        (hq, sq), d = _token_rows("q", q, T, dev), q.shape[2]
+        hq, d, sq = _token_rows("q", q, T, dev)
+        pq = q.data_ptr()
     if k is not None:
-        (hk, sk), d = _token_rows("k", k, T, dev), k.shape[2]
+        hkv, dk, sk = _token_rows("k", k, T, dev)
+        pk = k.data_ptr()
+        if d is None:
+            d = dk
+        elif d != dk:
+            raise ValueError("q and k must have the same head dimension")
     if v is not None:
-        (hv, sv), d = _token_rows("v", v, T, dev), v.shape[2]
-    if k is not None and v is not None and hk != hv:
-        raise ValueError("k and v must have the same heads")
-    hkv = hk or hv
-    if any(t is not None and t.shape[2] != d for t in (q, k)):
-        raise ValueError("q, k and v must have the same head dimension")
+        hv, dv, sv = _token_rows("v", v, T, dev)
+        pv = v.data_ptr()
+        if (k is not None and hv != hkv) or (d is not None and dv != d):
+            raise ValueError("k and v must have the same heads, q, k and v the same head dimension")
+        hkv, d = hv, dv
+    made = torch.uint8 if fp8 else torch.bfloat16
+    pcache = None
     if cache is not None:
         if slots is None or k is None or v is None:
             raise ValueError("a cache needs k, v and slots")
         _need("slots", slots, torch.int32, (T,), dev)
+        pslots = slots.data_ptr()
         if cache.kind != (dev, fp8, hkv, d):
             raise ValueError(f"the pages must be contiguous [P, page_size, {hkv}, {d}] on {dev} in "
                              f"{'e4m3' if fp8 else 'bf16'}, got (device, e4m3, heads, dim) {cache.kind}")
-    made = torch.uint8 if fp8 else torch.bfloat16
+        pcache = ctypes.byref(cache.desc)
+    else:
+        k_out = torch.empty((T, hkv, d), dtype=made, device=dev) if k_out is None and k is not None else k_out
+        v_out = torch.empty((T, hkv, d), dtype=made, device=dev) if v_out is None and v is not None else v_out
     if q_out is None:
         if q is not None:
             q_out = torch.empty((T, hq, d), dtype=made, device=dev)
+            pqo = q_out.data_ptr()
     else:
         _need("q_out", q_out, q_out.dtype if fp8 and q_out.dtype in FP8_DTYPES else made, (T, hq, d), dev)
-    if cache is None:
-        k_out = torch.empty((T, hkv, d), dtype=made, device=dev) if k_out is None and k is not None else k_out
-        v_out = torch.empty((T, hkv, d), dtype=made, device=dev) if v_out is None and v is not None else v_out
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None:
-            _need(name, t, t.dtype if fp8 and t.dtype in FP8_DTYPES else made, (T, hkv, d), dev)
+        pqo = q_out.data_ptr()
+    if k_out is not None:
+        _need("k_out", k_out, k_out.dtype if fp8 and k_out.dtype in FP8_DTYPES else made, (T, hkv, d), dev)
+        pko = k_out.data_ptr()
+    if v_out is not None:
+        _need("v_out", v_out, v_out.dtype if fp8 and v_out.dtype in FP8_DTYPES else made, (T, hkv, d), dev)
+        pvo = v_out.data_ptr()
+    pqs = pks = pvs = None
     if fp8:
-        for name, t, h in (("q_scale", q_scale, hq), ("k_scale", k_scale, hkv), ("v_scale", v_scale, hkv)):
-            if t is not None:
-                _need(name, t, torch.float32, (h,), dev)
+        if q_scale is not None:
+            _need("q_scale", q_scale, torch.float32, (hq,), dev)
+            pqs = q_scale.data_ptr()
+        if k_scale is not None:
+            _need("k_scale", k_scale, torch.float32, (hkv,), dev)
+            pks = k_scale.data_ptr()
+        if v_scale is not None:
+            _need("v_scale", v_scale, torch.float32, (hkv,), dev)
+            pvs = v_scale.data_ptr()
     elif q_scale is not None or k_scale is not None or v_scale is not None:
         raise ValueError("scales are for e4m3 outputs")
-    io = StemRopeIO(T, hq, hkv, d, STEM_FP8_E4M3 if fp8 else STEM_BF16, positions.data_ptr(), _ptr(slots), _ptr(q),
-                    _ptr(k), _ptr(v), sq, sk, sv, _ptr(q_scale), _ptr(k_scale), _ptr(v_scale), _ptr(q_out), _ptr(k_out),
-                    _ptr(v_out))
-    _run(dev, stream, "stem_rope", LIB.stem_rope, ctypes.byref(rope), ctypes.byref(io),
-         None if cache is None else ctypes.byref(cache.desc))
+    io = StemRopeIO(T, hq, hkv, 128 if d is None else d, STEM_FP8_E4M3 if fp8 else STEM_BF16, positions.data_ptr(),
+                    pslots, pq, pk, pv, sq, sk, sv, pqs, pks, pvs, pqo, pko, pvo)
+    _run(dev, stream, "stem_rope", LIB.stem_rope, ctypes.byref(rope), ctypes.byref(io), pcache)
     return q_out, k_out, v_out
 
 
@@ -597,6 +616,10 @@ class TreeQ:
     k_scale: torch.Tensor | None
     v_scale: torch.Tensor | None
     desc: StemTree
+
+    def __post_init__(self):
+        # (device, e4m3, KV heads, head dim): what the pages have to be
+        self.kind = (self.q.device, self.desc.dtype == STEM_FP8_E4M3, self.desc.num_kv_heads, self.desc.head_dim)
 
 
 def make_tree(q, cu_seqlens, kv_lens, num_kv_heads: int, mask=None, max_seq_tokens: int = 0, q_scale=None, k_scale=None,
@@ -637,14 +660,14 @@ def stem_tree_attn(tree: TreeQ, kv: PagedKV, out=None, lse=None, ws=None, stream
     """Attention of a step's queries over the paged cache: out bf16 [T, Hq, 128],
     lse fp32 [Hq, T], and the workspace (whose status word tells of bad lengths)."""
     q = tree.q
-    dev = q.device
-    T, hq, d = q.shape
     desc = tree.desc
-    if kv.kind != (dev, desc.dtype == STEM_FP8_E4M3, desc.num_kv_heads, d):
-        raise ValueError(f"the pages must be contiguous [P, page_size, {desc.num_kv_heads}, {d}] on {dev} in "
-                         f"{'e4m3' if desc.dtype else 'bf16'}, got (device, e4m3, heads, dim) {kv.kind}")
-    if kv.page_table.shape[0] < desc.num_seqs:
+    T, hq, d = q.shape
+    if kv.kind != tree.kind:
+        raise ValueError(f"the pages must be contiguous and of the queries' kind: (device, e4m3, KV heads, head dim) "
+                         f"{tree.kind}, got {kv.kind}")
+    if kv.page_table.shape[0] < tree.kv_lens.shape[0]:
         raise ValueError("page_table must have a row per sequence")
+    dev = tree.kind[0]
     if out is None:
         out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev)
     else:

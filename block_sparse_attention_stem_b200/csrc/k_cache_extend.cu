@@ -237,6 +237,10 @@ cudaError_t launch_cache_extend(const ExtendArgs& args, cudaStream_t stream) {
     e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
+  if (ctas == 1) {
+    cache_extend_kernel<<<1, kExtendThreads, smem, stream>>>(args);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kExtendThreads);

@@ -39,6 +39,7 @@ stem_status_t check_pool(int32_t page_size, int32_t num_pages) {
 // Angular frequency of every rotated pair in units of 2^-64 turns per position.
 void rope_turns(const stem_rope_t& r, RopeArgs* a) {
   constexpr long double kTwoPi = 6.283185307179586476925286766559005768L;
+  constexpr long double kTurns = 18446744073709551616.0L / kTwoPi;  // 2^64 to the turn
   const int half = r.rotary_dim / 2;
   double base = r.base;
   if (r.scaling == STEM_ROPE_NTK)
@@ -63,7 +64,7 @@ void rope_turns(const stem_rope_t& r, RopeArgs* a) {
       const double t = std::min(std::max((j - low) / (high - low), 0.0), 1.0);
       w = w / r.factor * t + w * (1.0 - t);
     }
-    a->turn[j] = static_cast<uint64_t>(w / kTwoPi * 18446744073709551616.0L);  // w <= 1: below 2^62
+    a->turn[j] = static_cast<uint64_t>(w * kTurns);  // w <= 1: below 2^62
   }
   double amp = r.amplitude;
   if (amp == 0.0) amp = r.scaling == STEM_ROPE_YARN ? 0.1 * std::log(r.factor) + 1.0 : 1.0;
