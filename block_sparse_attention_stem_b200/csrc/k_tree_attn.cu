@@ -110,27 +110,20 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
     if (sm.abort) sm.status = STEM_ERR_TIMEOUT_CODE;
     for (int x = 0; x < 4; ++x) sm.odd_v[x] = 0;
   }
-  const int64_t count = find_range<Cfg::kThreads>(a, range, sm.range, &sm.status);
-  if (threadIdx.x == 0) {
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&sm.q_full[b], 1);
-      mbar_init(&sm.q_empty[b], 1);
-      mbar_init(&sm.wide_full[b], Cfg::kWidenWarps);
-      mbar_init(&sm.s_full[b], 1);
-      mbar_init(&sm.p_full[b], 4);
-      mbar_init(&sm.pv_done[b], 1);
-    }
-    for (int b = 0; b < Cfg::kKSlots; ++b) {
-      mbar_init(&sm.k_full[b], 1);
-      mbar_init(&sm.k_empty[b], 1);
-    }
-    for (int b = 0; b < Cfg::kVSlots; ++b) {
-      mbar_init(&sm.v_full[b], 1);
-      mbar_init(&sm.v_empty[b], kFp8 ? Cfg::kWidenWarps : 1);
-    }
-    mbar_init(&sm.drain, 1);
+  // the barriers, a lane each, and the tensor maps' fetch, before earlier kernels are waited for
+  constexpr int kBars = 13 + 2 * Cfg::kKSlots + 2 * Cfg::kVSlots;
+  static_assert(offsetof(TreeSmem<kFp8>, drain) == offsetof(TreeSmem<kFp8>, q_full) + (kBars - 1) * 8, "barriers in a row");
+  if (warp == kMmaIssuer && lane < kBars) {
+    uint64_t* bar = &sm.q_full[0] + lane;
+    uint32_t count = 1;
+    if (bar >= &sm.p_full[0] && bar < &sm.p_full[2]) count = 4;
+    if (kFp8 && bar >= &sm.wide_full[0] && bar < &sm.wide_full[2]) count = Cfg::kWidenWarps;
+    if (kFp8 && bar >= &sm.v_empty[0] && bar < &sm.v_empty[Cfg::kVSlots]) count = Cfg::kWidenWarps;
+    mbar_init(bar, count);
     fence_mbar_init();
   }
+  if (warp == kProducer && lane < 3) tma_prefetch_desc(lane == 0 ? &maps.k_pool : lane == 1 ? &maps.q : &maps.v_pool);
+  const int64_t count = find_range<Cfg::kThreads>(a, range, sm.range, &sm.status);
   if (count == 0) {
     __syncthreads();
     if (threadIdx.x == 0) a.cta_status[blockIdx.x] = sm.status;
@@ -159,11 +152,6 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
     // of V by `ahead` units.  While V_h is the next V, the products up to
     // S_{h+1} can complete, and the Q tile of K_{h+ahead-1} may have to wait for
     // S_{h+ahead-1-qbufs} (items of one unit): hence ahead <= 2 + qbufs.
-    if (lane == 0) {
-      tma_prefetch_desc(&maps.q);
-      tma_prefetch_desc(&maps.k_pool);
-      tma_prefetch_desc(&maps.v_pool);
-    }
     struct Stream {
       Walk w;
       int u, rows, h, slot, round;

@@ -142,26 +142,16 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
     sm.abort = (smem_u32(smem_raw) & 1023u) != 0;  // the swizzled tiles need this alignment
     if (sm.abort) sm.status = STEM_ERR_TIMEOUT_CODE;
     for (int x = 0; x < 4; ++x) sm.odd_v[x] = 0;
-    for (int b = 0; b < kQBufs; ++b) {
-      mbar_init(&sm.q_full[b], 1);
-      mbar_init(&sm.q_empty[b], 1);
-    }
-    for (int b = 0; b < Cfg::kSlots; ++b) {
-      mbar_init(&sm.k_full[b], 1);
-      mbar_init(&sm.k_empty[b], 1);
-    }
-    for (int b = 0; b < Cfg::kSlots; ++b) {
-      mbar_init(&sm.v_full[b], 1);
-      mbar_init(&sm.v_empty[b], 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&sm.s_full[b], 1);
-      mbar_init(&sm.p_full[b], 4);
-      mbar_init(&sm.pv_done[b], 1);
-    }
-    mbar_init(&sm.drain, 1);
+  }
+  // the barriers, a lane each, and the tensor maps' fetch, before earlier kernels are waited for
+  constexpr int kBars = 2 * kQBufs + 4 * Cfg::kSlots + 7;
+  static_assert(offsetof(NarrowSmem<kFp8>, drain) == offsetof(NarrowSmem<kFp8>, q_full) + (kBars - 1) * 8, "barriers in a row");
+  if (warp == kMmaIssuer && lane < kBars) {
+    uint64_t* bar = &sm.q_full[0] + lane;
+    mbar_init(bar, bar == &sm.p_full[0] || bar == &sm.p_full[1] ? 4 : 1);
     fence_mbar_init();
   }
+  if (warp == kProducer && lane < 3) tma_prefetch_desc(lane == 0 ? &maps.k_pool : lane == 1 ? &maps.q : &maps.v_pool);
   const int64_t count = find_range<kThreads>(a, blockIdx.x, sm.range, &sm.status);
   if (count == 0) {
     __syncthreads();
@@ -189,11 +179,6 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
     // complete, and the Q tile of K_{h+ahead-1} may have to wait for
     // S_{h+ahead-1-kQBufs} (items of one unit): ahead <= 2 + kQBufs.
     constexpr int kAhead = Cfg::kSlots < 2 + kQBufs ? Cfg::kSlots : 2 + kQBufs;
-    if (lane == 0) {
-      tma_prefetch_desc(&maps.q);
-      tma_prefetch_desc(&maps.k_pool);
-      tma_prefetch_desc(&maps.v_pool);
-    }
     struct Stream {
       Walk w;
       int u, rows, h, slot, round;
