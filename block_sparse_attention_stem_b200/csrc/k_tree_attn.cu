@@ -84,6 +84,16 @@ struct TreeSmem {
   int odd_v[4];  // [item % 4]: item + 1 when a non-finite element of V was zeroed in it
 };
 
+// Four e4m3 bytes as two f16 pairs (exact).
+__device__ __forceinline__ void widen_e4m3x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+
 // Scores of keys that are not seen become -inf.
 __device__ __forceinline__ void hide(uint32_t (&rr)[32], uint32_t see) {
 #pragma unroll
@@ -310,8 +320,15 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
   } else if (kFp8 && warp >= kWidenWarp) {
     // ------------------------------------------------------------ V -> f16
     if constexpr (kFp8) {
+      // Thread: 16-byte chunk c of rows r, r + 16, r + 32, r + 48, whose 16 elements are
+      // chunks 2 (c % 4) and + 1 of slab c / 4 of the wide tile.  The lanes of one slab
+      // take even rows while those of the other take odd ones, so that the eight
+      // lanes of a shared-memory phase write eight different chunk positions.
       const int t = (warp - kWidenWarp) * 32 + lane;
-      const int c = t & 7;  // 16-byte chunk of the e4m3 row
+      const int c = t & 7, r = (t >> 3) ^ (c >> 2);
+      const int from = r * 128 + ((c ^ (r & 7)) << 4);
+      const int to = (c >> 2) * (kUnit * 128) + r * 128;
+      const int to0 = to + (((2 * (c & 3)) ^ (r & 7)) << 4), to1 = to + (((2 * (c & 3) + 1) ^ (r & 7)) << 4);
       int h = 0;
       bool ok = !*abort;
       for (int item = 0; ok && wk.next(a, tile); ++item) {
@@ -321,25 +338,23 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
                (h < 2 || mbar_wait(&sm.pv_done[h & 1], ((h - 2) >> 1) & 1, abort, status));
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint8_t* src = sm.v[slot];
-          uint8_t* dst = sm.wide[h & 1] + (c >> 2) * (kUnit * 128);
+          const uint8_t* src = sm.v[slot] + from;
+          uint8_t* dst = sm.wide[h & 1];
           const bool check = (u + 1) * kUnit > wk.q.ctx;
           const int end = wk.q.kv - u * kUnit;  // rows from here on are behind the keys
           bool odd = false;
 #pragma unroll 1
-          for (int r = t >> 3; r < kUnit; r += Cfg::kWidenWarps * 4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
-            uint32_t w[8];
+          for (int step = 0; step < kUnit * 128; step += Cfg::kWidenWarps * 4 * 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + step);
             const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+            uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              w[2 * e] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[e] & 0xffffu));
-              w[2 * e + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[e] >> 16));
-            }
+            for (int e = 0; e < 4; ++e) widen_e4m3x4(in[e], w[2 * e], w[2 * e + 1]);
             if (check) {
+              const bool behind = r + step / 128 >= end;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                if (r >= end) w[e] = 0u;
+                if (behind) w[e] = 0u;
                 if ((w[e] & 0x7c00u) == 0x7c00u) {
                   w[e] &= 0xffff0000u;
                   odd = true;
@@ -350,14 +365,8 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
                 }
               }
             }
-            // elements 16 c .. 16 c + 15: chunks 2 (c % 4) and + 1 of slab c / 4;
-            // the two slabs' lanes write opposite halves first (other banks)
-            const int o = 2 * (c & 3), f = c >> 2;
-            uint8_t* row = dst + r * 128;
-            *reinterpret_cast<uint4*>(row + (((o + f) ^ (r & 7)) << 4)) =
-                f ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(row + (((o + 1 - f) ^ (r & 7)) << 4)) =
-                f ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(w[4], w[5], w[6], w[7]);
+            *reinterpret_cast<uint4*>(dst + to0 + step) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + to1 + step) = make_uint4(w[4], w[5], w[6], w[7]);
           }
           if (odd) sm.odd_v[item & 3] = item + 1;  // at most two items ahead of the epilogue
           fence_async_smem();
