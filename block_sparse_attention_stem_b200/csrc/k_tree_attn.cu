@@ -1,5 +1,6 @@
 // k_tree_attn.cu — attention of drafted trees, single tokens or causal chunks
-// over the paged cache.
+// over the paged cache (more than 16 query rows per sequence and KV head; fewer:
+// k_tree_narrow.cu), and the kernels that join the pieces of both.
 //
 //   O = sum_u exp2(c q.k_u - m) v_u / l,  m the running reference max, l the sum
 //
@@ -12,28 +13,39 @@
 //   P = exp2(..)  the softmax warps (thread = row = TMEM lane), over S
 //   O += P V      tcgen05.mma, P from TMEM, V from SMEM; O stays in TMEM
 //
-// Bound: every K/V byte once from HBM; a tile needs 4 * 128 FLOP per byte, so
-// the tensor cores are far from busy.  What matters is that all SMs stream all
-// the time, whatever the lengths: the units of all (sequence, KV head) items are
-// laid end to end and cut into equal ranges, one per CTA (two CTAs per SM).  A
-// range may hold the end of one item, several whole ones and the start of
-// another; whole ones are written at once, the at most two pieces go to the
-// workspace (fp32 O, m, l) and a second kernel joins them in range order.  The
-// cuts depend on the lengths alone, so results repeat bit for bit.  Sequences
+// Work split: all SMs have to stream all the time, whatever the lengths.  The
+// items (sequence, KV head) are laid end to end and cut into equal ranges, one
+// per CTA (two CTAs per SM); an item counts a few units more than it has, for
+// its start and its epilogue.  A range may hold the end of one item, several
+// whole ones and the start of another; whole ones are written at once, the at
+// most two pieces go to the workspace (fp32 O, m, l; dim by dim, so that a
+// warp's 32 rows are one line) and a second kernel joins them in range order.
+// The cuts depend on the lengths alone, so results repeat bit for bit.  Sequences
 // with more than 128 rows have several tiles: the CTAs of one range (blockIdx =
 // range * tiles + tile) read the same keys at the same time, from L2.
 //
 // bf16: P is kept as a sum of two bf16 (15 significant bits; they fill the 64
 // columns of S exactly), so its rounding does not add to the output's: with a
 // single bf16 P the error of a long average is as large as the output rounding
-// itself.  The second product is free while HBM is the bound.  e4m3: Q K^T on
-// the e4m3 operands, P in f16, V widened to f16 (exact) by warps of their own.
+// itself.  e4m3: Q K^T on the e4m3 operands, P in f16, V widened to f16 (exact)
+// by warps of their own.
 //
 // Masked keys: S is replaced by -inf, so nothing in K matters.  A product 0 * v
 // would still carry a NaN or infinity of V into rows that do not see the key,
 // so in units that hold new tokens or the end of the sequence, rows of V behind
 // the end are zeroed in SMEM and non-finite elements of new tokens too; rows
 // that do see such an element get it added in the epilogue.
+//
+// What bounds it.  bf16, one full tile: HBM (eight 32-token trees over 16-32K,
+// 811 MB: the kernel reads 5.67 TB/s, 143 us; 163 us with the join, about 200
+// when the power cap lowers the clock; tensor pipe 57%).  e4m3: instruction
+// issue (51%, four warps per scheduler): exponentials, and widening V, whose bytes
+// HBM would deliver in half the time (sixteen 33-63-token trees, two tiles: 192
+// us).  The roles share one instruction cache: rolling the exponentials and the
+// widening loop took 279 to 222 us, four widening warps at 96 registers 213,
+// fixed addresses without bank conflicts 206 to 192.  Widening by moving bits
+// instead of cvt measured 316 us, keeping the scores in registers with two
+// widening warps 195.
 //
 // 192 threads (320 for e4m3):
 //   warps 0-3  softmax, epilogue (TMEM lane quarter = warp)
@@ -857,7 +869,8 @@ static cudaError_t launch_tree_t(const TreeMaps& maps, const TreeArgs& args, cud
   if (args.ranges == 1)  // one range holds everything: nothing is cut, only the status is left
     return launch_after(tree_join_rows_kernel, dim3(1), kJoinWarps * 32, 0, stream, j, grid, 0);
   if (args.unit_keys == kUnit) {
-    // few items: more blocks, with fewer dims each
+    // few items: more blocks, with fewer dims each (four 32-token trees over 4K: 34 us, with
+    // 16 dims a warp 41)
     const int groups = args.tiles * (args.part_rows / 32);
     if (groups * items >= 4 * 148)
       return launch_after(tree_join_dims_kernel<16>, dim3(groups, gy), kJoinWarps * 32, 0, stream, j, grid);

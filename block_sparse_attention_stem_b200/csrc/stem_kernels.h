@@ -173,8 +173,19 @@ struct TreeArgs {
 };
 constexpr int kTreeRanges = 296;    // two CTAs on each of 148 SMs
 constexpr int kNarrowRanges = 148;  // one CTA per SM (e4m3: twice as many, two per SM)
-constexpr int kNarrowRows = 16;     // query rows (tokens * group) up to which the narrow kernel is used
-constexpr int kNarrowItemUnits = 2, kTreeItemUnits = 5, kNarrowMinRange = 4, kTreeMinRange = 6;
+// Query rows (tokens * group) up to which the narrow kernel is used.  16 rows over
+// 16K keys of 16 sequences: 164 us, against 192 us in the 128-row kernel for 64
+// rows, which costs the same for fewer; for 32 rows a narrow kernel with 32
+// columns took 211 us (e4m3 241), the 128-row kernel 185 (153).
+constexpr int kNarrowRows = 16;
+// Units that an item counts beyond its own.  64 tokens over 1 to 8K keys (narrow):
+// none 192 us, one 176, two or three 168; eight 32-token trees over 16-32K: none
+// 167 us, two 174 and four or six 172 in an earlier state, five 165.
+constexpr int kNarrowItemUnits = 2, kTreeItemUnits = 5;
+// Shortest range, in units.  One token over 300 keys: 13.7 us with three, 15.3
+// with four, 19.0 with eight; a 32-token tree over 1000: 19.1, 20.2 (six), 23.4
+// (twelve); nothing else changes.
+constexpr int kNarrowMinRange = 3, kTreeMinRange = 3;
 cudaError_t launch_tree_attn(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
 cudaError_t launch_tree_narrow(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream);
 
