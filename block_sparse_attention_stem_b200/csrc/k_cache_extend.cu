@@ -8,7 +8,7 @@
 // the same tokens spread over many sequences.
 //
 // Measured on the GPU: four requests with a token each 3.9 us, 256 trees of 17 to
-// 64 tokens 9.5 us, 160K prompt tokens 14.7 us (16 CTAs; 8 took 25 us).
+// 64 tokens 9.5 us, 213K prompt tokens 14.7 us (16 CTAs; 8 took 25 us).
 //
 // One cluster: every CTA reads all lengths and repeats the (short) scans, the
 // cluster's barrier separates those reads from the writes, so the outputs may

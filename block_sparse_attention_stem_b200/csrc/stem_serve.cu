@@ -114,6 +114,8 @@ stem_status_t tree_layout(const stem_tree_t* t, TreeLayout* out) {
   if (t->head_dim != kHeadDim) return t->head_dim < 1 ? STEM_ERR_INVALID_ARG : STEM_ERR_UNSUPPORTED;
   if (t->mask ? t->mask_words < 1 : t->mask_words < 0) return STEM_ERR_INVALID_ARG;
   if (!(t->softmax_scale >= 0.0) || !std::isfinite(t->softmax_scale)) return STEM_ERR_INVALID_ARG;
+  if (t->total_tokens > (1 << 30) || static_cast<int64_t>(t->num_seqs) * t->num_kv_heads > (1 << 30))
+    return STEM_ERR_UNSUPPORTED;
   TreeLayout l{};
   l.group = t->num_q_heads / t->num_kv_heads;
   if (l.group > 128) return STEM_ERR_UNSUPPORTED;
@@ -150,13 +152,16 @@ stem_status_t stem_cache_extend(const stem_cache_step_t* step, int32_t* page_tab
     return STEM_ERR_INVALID_ARG;
   stem_status_t st = check_pool(step->page_size, step->num_pages);
   if (st != STEM_OK) return st;
-  if (static_cast<int64_t>(step->num_seqs) * step->max_pages_per_seq > INT32_MAX) return STEM_ERR_INVALID_ARG;
+  // counters of tokens and table entries step past their ends in 32 bits
+  if (step->max_tokens > (1 << 30) || static_cast<int64_t>(step->num_seqs) * step->max_pages_per_seq > (1 << 30))
+    return STEM_ERR_INVALID_ARG;
   if (!step->cache_lens || !step->new_lens || !step->held_pages || !step->cursor ||
       (!step->free_pages && step->num_free > 0))
     return STEM_ERR_INVALID_ARG;
   if (!page_table || !held_out || !cursor_out || !cu_seqlens || !kv_lens || !ws) return STEM_ERR_INVALID_ARG;
   if (step->max_tokens > 0 && (!slots || !positions)) return STEM_ERR_INVALID_ARG;
   if ((step->parents != nullptr) != (mask != nullptr) || (mask && step->mask_words < 1)) return STEM_ERR_INVALID_ARG;
+  if (!aligned(ws, 4)) return STEM_ERR_MISALIGNED;
   if (ws_bytes < kStatusBytes) return STEM_ERR_WORKSPACE_TOO_SMALL;
   if (step->num_seqs > kMaxExtendSeqs) return STEM_ERR_UNSUPPORTED;
   StageRange nvtx_range("stem: cache extend");

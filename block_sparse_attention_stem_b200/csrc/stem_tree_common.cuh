@@ -76,7 +76,7 @@ struct Walk {
   // the next item whose sequence has this tile; false at the end of the range
   __device__ __forceinline__ bool next(const TreeArgs& a, int tile) {
     while (left > 0) {
-      if (hk == a.hkv) {
+      if (hk >= a.hkv) {
         hk = 0;
         do {
           if (++s >= a.seqs) {  // the lengths changed under the call
@@ -241,7 +241,7 @@ __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, Rang
   if (count > 0 && before <= u0 && u0 < before + mine) {
     int64_t at = before;
     int s = s_beg;
-    for (;; ++s) {
+    for (; s + 1 < s_end; ++s) {
       const int64_t more = seq_length(a, seq_shape(a, s));
       if (u0 < at + more) break;
       at += more;

@@ -342,10 +342,10 @@ STEM_API stem_status_t stem_noalloc_read_device_status(stem_stream_t stream, ste
  * cache and adds new_lens[s].  All pointers are device pointers. */
 typedef struct {
   int32_t num_seqs;           /* S, 1 .. 8192 (STEM_ERR_UNSUPPORTED beyond) */
-  int32_t max_tokens;         /* length of the per-token outputs; >= the sum of new_lens */
+  int32_t max_tokens;         /* length of the per-token outputs; >= the sum of new_lens; at most 2^30 */
   int32_t page_size;          /* tokens per page; a multiple of 64 */
   int32_t num_pages;          /* pages in the pool (num_pages * page_size < 2^31) */
-  int32_t max_pages_per_seq;  /* row length of the page table (S * max_pages_per_seq < 2^31) */
+  int32_t max_pages_per_seq;  /* row length of the page table (S * max_pages_per_seq at most 2^30) */
   int32_t num_free;           /* length of free_pages */
   int32_t mask_words;         /* with parents: 32-bit words per token of the mask, >= 1 */
   const int32_t* cache_lens;  /* [S] */
@@ -432,8 +432,9 @@ typedef struct {
   int32_t head_dim;          /* 128 */
   int32_t out_dtype;         /* stem_dtype_t of every output and of the pages */
   const int32_t* positions;  /* [T]; any int32 */
-  const int32_t* slots;      /* [T] with a cache: row of the pool, -1 (or any row outside the pool) to
-                                skip the token; no row may occur twice */
+  const int32_t* slots;      /* [T] with a cache: row of the pool, -1 (or any row outside the pool): not
+                                stored there (packed outputs are written all the same); no row may
+                                occur twice */
   const void* q;             /* NULL with q_out NULL */
   const void* k;             /* NULL with k_out NULL and no cache */
   const void* v;             /* NULL with v_out NULL and no cache */
@@ -464,7 +465,7 @@ STEM_API stem_status_t stem_rope(const stem_rope_t* rope, const stem_rope_io_t* 
  * of its kv_lens[s] cached ones (n of them; n = 1 is plain decoding). */
 typedef struct {
   int32_t dtype;              /* stem_dtype_t of q and of the pages */
-  int32_t num_seqs;           /* >= 1 */
+  int32_t num_seqs;           /* >= 1; num_seqs * num_kv_heads and total_tokens at most 2^30 */
   int32_t total_tokens;       /* rows of q, out and lse: >= cu_seqlens[num_seqs] */
   int32_t max_seq_tokens;     /* no sequence has more queries than this; 0 selects total_tokens */
   int32_t num_q_heads;        /* Hq, a multiple of Hkv, at most 128 Hkv */
@@ -503,7 +504,9 @@ STEM_API stem_status_t stem_tree_plan(const stem_tree_t* tree, size_t* ws_bytes)
  * total_tokens (the sequence is skipped), a sequence with more than
  * max_seq_tokens queries (those beyond are skipped), a negative kv_lens (taken
  * as 0) or one past the table's row (the keys beyond are not seen);
- * STEM_ERR_TIMEOUT.  Two launches; the workspace holds nothing between calls. */
+ * STEM_ERR_TIMEOUT.  Two launches; the workspace (16-byte aligned) holds nothing
+ * between calls, so calls in stream order may share one; calls that may overlap
+ * on the GPU need one each. */
 STEM_API stem_status_t stem_tree_attn(const stem_tree_t* tree, const stem_paged_kv_t* kv, void* out, float* lse,
                                       void* ws, size_t ws_bytes, stem_stream_t stream);
 

@@ -193,6 +193,43 @@ def test_long_context_split_over_all_ranges(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,hq", [(60, 5), (45, 3), (20, 7), (3, 5), (1, 13)])
+def test_cut_items_of_odd_groups(n, hq, fp8):
+    """Tiles of fewer than 128 rows, several of them, cut over many ranges."""
+    Case([n, 1], [3000, 2000], hq, 1, fp8, tree=True, seed=n + hq).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_very_long_context(fp8):
+    """700,000 keys: one sequence and KV head over every range; rows checked on the GPU in fp64."""
+    L, hq = 700_001, 4
+    g = torch.Generator("cuda").manual_seed(31)
+    P = -(-L // 64)
+    sc = [torch.full((h,), 0.01, device="cuda") for h in (hq, 1, 1)] if fp8 else [None] * 3
+    x = [torch.randn(n, h, 128, generator=g, device="cuda") for n, h in ((1, hq), (P * 64, 1), (P * 64, 1))]
+    enc = [(y / 0.01).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else y.to(torch.bfloat16) for y in x]
+    dec = [y.view(torch.float8_e4m3fn).double() * float(s[0]) if fp8 else y.double() for y, s in zip(enc, sc)]
+    perm = torch.randperm(P, generator=g, device="cuda")
+    pools = [torch.empty_like(y).view(P, 64, 1, 128) for y in enc[1:]]
+    for p, y in zip(pools, enc[1:]):
+        p[perm] = y.view(P, 64, 1, 128)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    tree = b.make_tree(enc[0], torch.tensor([0, 1], **i32), torch.tensor([L], **i32), 1, max_seq_tokens=1,
+                       q_scale=sc[0], k_scale=sc[1], v_scale=sc[2])
+    out, lse, ws = b.stem_tree_attn(tree, b.paged_kv(*pools, perm.to(torch.int32)[None].contiguous(), 64))
+    assert b.stem_read_device_status(ws) == 0
+    s = dec[0][0] @ dec[1][:L, 0].T / 128 ** 0.5
+    z = torch.logsumexp(s, 1)
+    p = torch.exp(s - z[:, None])
+    o, av = p @ dec[2][:L, 0], p @ dec[2][:L, 0].abs()
+    logit = 136 * 2.0 ** -24 * float((dec[0][0].abs() @ dec[1][:L, 0].abs().T).max()) / 128 ** 0.5
+    # at most 296 pieces of 2400 keys, summed apart and then joined
+    w = 2 * logit + 2.0 ** -20 + (2.0 ** -10 if fp8 else 2.0 ** -15) + 2 * (4800 + 296) * 2.0 ** -24
+    assert torch.all((out[0].double() - o).abs() <= 2.0 ** -8 * o.abs() + w * av)
+    assert torch.all((lse[:, 0].double() - z).abs() <= logit + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_rows_whose_mask_leaves_nothing(fp8):
     c = Case([6, 40], [0, 0], 4, 2, fp8, tree=True, seed=12)
     c.mask[[1, 4, 9, 45]] = 0

@@ -34,7 +34,8 @@ def extend(desc, mask=None, ws_bytes=256, **null):
     (dict(num_seqs=0), INVALID), (dict(num_seqs=8193), UNSUPPORTED), (dict(max_tokens=-1), INVALID),
     (dict(page_size=0), INVALID), (dict(page_size=96), INVALID), (dict(num_pages=0), INVALID),
     (dict(num_pages=1 << 25), INVALID), (dict(max_pages_per_seq=0), INVALID),
-    (dict(num_seqs=4096, max_pages_per_seq=1 << 20), INVALID), (dict(num_free=-1), INVALID),
+    (dict(num_seqs=4096, max_pages_per_seq=1 << 20), INVALID), (dict(max_tokens=(1 << 30) + 1), INVALID),
+    (dict(num_seqs=2, max_pages_per_seq=(1 << 29) + 1), INVALID), (dict(num_free=-1), INVALID),
     (dict(cache_lens=None), INVALID), (dict(new_lens=None), INVALID), (dict(held_pages=None), INVALID),
     (dict(cursor=None), INVALID), (dict(free_pages=None), INVALID),
     (dict(parents=FAKE, mask_words=1), INVALID),  # parents without a mask
@@ -115,6 +116,7 @@ def plan(desc):
     (dict(dtype=2), INVALID), (dict(num_seqs=0), INVALID), (dict(total_tokens=-1), INVALID),
     (dict(max_seq_tokens=-1), INVALID), (dict(num_q_heads=7), INVALID), (dict(num_kv_heads=0), INVALID),
     (dict(num_q_heads=129, num_kv_heads=1), UNSUPPORTED), (dict(head_dim=64), UNSUPPORTED), (dict(head_dim=0), INVALID),
+    (dict(total_tokens=(1 << 30) + 1), UNSUPPORTED), (dict(num_seqs=1 << 30), UNSUPPORTED),
     (dict(mask=FAKE, mask_words=0), INVALID), (dict(softmax_scale=-1.0), INVALID), (dict(softmax_scale=math.nan), INVALID),
 ])
 def test_tree_plan_refuses(kw, code):
