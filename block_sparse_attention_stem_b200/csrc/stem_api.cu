@@ -242,24 +242,22 @@ bool encode_seq_map(CUtensorMap* m, const void* base, bool fp8, int heads, int t
 }  // namespace
 
 namespace stem {
-bool encode_pool_map(CUtensorMap* m, const void* base, bool fp8, int heads, int rows, int box_rows) {
-  return encode_seq_map(m, base, fp8, heads, 0, rows, box_rows, 1);
-}
-
-bool encode_query_map(CUtensorMap* m, const void* base, bool fp8, int heads, int tokens, int box_heads,
-                      int box_tokens) {
+bool encode_rows_map(CUtensorMap* m, const void* base, bool fp8, int heads, int rows, int box_heads, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const size_t elt = fp8 ? 1 : 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(heads),
-                        static_cast<cuuint64_t>(tokens)};
+                        static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim * elt), static_cast<cuuint64_t>(heads * kHeadDim * elt)};
   cuuint32_t box[3] = {static_cast<cuuint32_t>(fp8 ? 128 : 64), static_cast<cuuint32_t>(box_heads),
-                       static_cast<cuuint32_t>(box_tokens)};
+                       static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[3] = {1u, 1u, 1u};
+  // L2 fetches whole head rows, no more: a row of e4m3 is 128 bytes, its neighbour another head's
   CUresult r = fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_SWIZZLE_128B,
+                  fp8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 }  // namespace stem

@@ -107,12 +107,9 @@ cudaError_t launch_vwiden(const void* v8, uint16_t* v16, int total_tokens, int h
 
 // ---- the paged cache (k_cache_extend.cu, k_rope.cu, k_tree_attn.cu)
 
-// 3-D maps of a whole [rows, heads, 128] page pool (box: box_rows rows of one
-// head) and of [tokens, heads, 128] queries (box: box_heads heads of
-// box_tokens tokens, token-major), 128-byte swizzle, one 128-byte slab wide.
-bool encode_pool_map(CUtensorMap* m, const void* base, bool fp8, int heads, int rows, int box_rows);
-bool encode_query_map(CUtensorMap* m, const void* base, bool fp8, int heads, int tokens, int box_heads,
-                      int box_tokens);
+// 3-D map of [rows, heads, 128] (a page pool or queries), box: box_heads heads of
+// box_rows rows, row-major, 128-byte swizzle, one 128-byte slab wide.
+bool encode_rows_map(CUtensorMap* m, const void* base, bool fp8, int heads, int rows, int box_heads, int box_rows);
 
 constexpr int kMaxExtendSeqs = 8192;  // sequences of one stem_cache_extend (16 B of SMEM each)
 struct ExtendArgs {

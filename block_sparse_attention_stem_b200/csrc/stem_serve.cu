@@ -274,9 +274,9 @@ stem_status_t stem_tree_attn(const stem_tree_t* tree, const stem_paged_kv_t* kv,
   StageRange nvtx_range("stem: tree attention");
   TreeMaps maps;
   const int rows = kv->num_pages * kv->page_size;
-  if (!encode_query_map(&maps.q, tree->q, fp8, tree->num_q_heads, tree->total_tokens, l.group, l.box_tokens) ||
-      !encode_pool_map(&maps.k_pool, kv->k_pages, fp8, tree->num_kv_heads, rows, 64) ||
-      !encode_pool_map(&maps.v_pool, kv->v_pages, fp8, tree->num_kv_heads, rows, 64))
+  if (!encode_rows_map(&maps.q, tree->q, fp8, tree->num_q_heads, tree->total_tokens, l.group, l.box_tokens) ||
+      !encode_rows_map(&maps.k_pool, kv->k_pages, fp8, tree->num_kv_heads, rows, 1, 64) ||
+      !encode_rows_map(&maps.v_pool, kv->v_pages, fp8, tree->num_kv_heads, rows, 1, 64))
     return STEM_ERR_CUDA;
   uint8_t* w = static_cast<uint8_t*>(ws);
   TreeArgs a{};
