@@ -123,7 +123,6 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
   TreeSmem<kFp8>& sm = *reinterpret_cast<TreeSmem<kFp8>*>(smem_raw);
   const int warp = warp_id(), lane = lane_id();
   const int range = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- where this range starts: prefix sum of the sequences' units
   if (threadIdx.x == 0) {

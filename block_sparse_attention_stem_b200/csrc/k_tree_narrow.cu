@@ -135,7 +135,6 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   NarrowSmem<kFp8>& sm = *reinterpret_cast<NarrowSmem<kFp8>*>(smem_raw);
   const int warp = warp_id(), lane = lane_id();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
     sm.status = 0;
