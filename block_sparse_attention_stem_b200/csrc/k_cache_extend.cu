@@ -8,7 +8,7 @@
 // the same tokens spread over many sequences.
 //
 // Measured on the GPU: four requests with a token each 3.9 us, 256 trees of 17 to
-// 64 tokens 9.5 us, 213K prompt tokens 14.7 us (16 CTAs; 8 took 25 us).
+// 64 tokens 9.4 us (with eight CTAs at most 13.4), 213K prompt tokens 13.3 us.
 //
 // One cluster: every CTA reads all lengths and repeats the (short) scans, the
 // cluster's barrier separates those reads from the writes, so the outputs may
@@ -25,7 +25,6 @@ namespace stem {
 namespace {
 
 constexpr int kExtendThreads = 1024;
-constexpr int kRun = 4;  // consecutive tokens of a thread in a large step without trees
 
 // Exclusive prefix sum of one value per thread over the block; *total gets the
 // sum.  `scratch`: 33 words, free for reuse after the call's last barrier.
@@ -150,76 +149,62 @@ __global__ void __launch_bounds__(kExtendThreads, 1) cache_extend_kernel(const E
     }
     a.page_table[static_cast<size_t>(s) * a.max_pages + held[s] + (e - tp[s])] = page;
   }
-  // tokens: slot, position and the bits of the ancestors; neighbours stay in one
-  // sequence and page most of the time, so a thread takes a few in a row
-  const int per = a.mask == nullptr && a.max_tokens >= kRun * size * kExtendThreads ? kRun : 1;
-  for (int t0 = (rank * kExtendThreads + tid) * per; t0 < a.max_tokens; t0 += size * kExtendThreads * per) {
-    int s = t0 < T ? find_last(cu, S, t0) : S;
-    uint32_t pg = 0xffffffffu;  // page whose number is in `page`
-    int page = -1;
-    for (int t = t0; t < min(t0 + per, a.max_tokens); ++t) {
-      int slot = -1, pos = 0, cur = -1;
-      const int32_t* par = a.parents;
-      if (t < T) {
-        while (s + 1 < S && cu[s + 1] <= t) {
-          ++s;
-          pg = 0xffffffffu;
-        }
-        const int i = t - cu[s];
-        const uint32_t p = static_cast<uint32_t>(clen[s]) + static_cast<uint32_t>(i);  // < 2^32
-        pos = static_cast<int>(min(p, 0x7fffffffu));
-        const uint32_t at = p / static_cast<uint32_t>(ps);
-        if (at != pg && at < static_cast<uint32_t>(a.max_pages)) {
-          pg = at;
-          page = -1;
-          const int e = static_cast<int>(pg) - held[s];
-          if (e < 0) page = a.page_table[static_cast<size_t>(s) * a.max_pages + pg];  // entries < held are not written
-          else if (tp[s] + e < avail) page = __ldg(a.free_pages + cursor + tp[s] + e);
-          if (page < 0 || page >= a.num_pages) {
-            bad |= e < 0 || tp[s] + e < avail;
-            page = -1;
-          }
-        }
-        if (at == pg && page >= 0) slot = page * ps + static_cast<int>(p - pg * static_cast<uint32_t>(ps));
-        if (par != nullptr) {
-          par += cu[s];
-          cur = i;
-          pos = clen[s];
-        }
+  // tokens: slot, position and the bits of the ancestors
+  for (int t = rank * kExtendThreads + tid; t < a.max_tokens; t += size * kExtendThreads) {
+    int slot = -1, pos = 0, cur = -1;
+    const int32_t* par = a.parents;
+    if (t < T) {
+      const int s = find_last(cu, S, t);
+      const int i = t - cu[s];
+      const uint32_t p = static_cast<uint32_t>(clen[s]) + static_cast<uint32_t>(i);  // < 2^32
+      pos = static_cast<int>(min(p, 0x7fffffffu));
+      const uint32_t pg = p / static_cast<uint32_t>(ps);
+      if (pg < static_cast<uint32_t>(a.max_pages)) {
+        const int e = static_cast<int>(pg) - held[s];
+        int page = -1;
+        if (e < 0) page = a.page_table[static_cast<size_t>(s) * a.max_pages + pg];  // entries < held are not written
+        else if (tp[s] + e < avail) page = __ldg(a.free_pages + cursor + tp[s] + e);
+        if (page >= 0 && page < a.num_pages) slot = page * ps + static_cast<int>(p - pg * static_cast<uint32_t>(ps));
+        else bad |= e < 0 || tp[s] + e < avail;
       }
-      a.slots[t] = slot;
-      if (a.mask != nullptr) {
-        // ancestors come in descending order, so the words are finished one by one from the last
-        uint32_t* row = a.mask + static_cast<size_t>(t) * a.mask_words;
-        int w = a.mask_words - 1, depth = -1;
-        uint32_t bits = 0;
-        while (cur >= 0) {
-          ++depth;
-          const int cw = cur >> 5;
-          if (cw >= a.mask_words) {
-            bad = true;
-          } else {
-            for (; w > cw; --w) {
-              row[w] = bits;
-              bits = 0;
-            }
-            bits |= 1u << (cur & 31);
-          }
-          const int up = __ldg(par + cur);
-          if (up >= cur || up < -1) {
-            bad = true;
-            break;
-          }
-          cur = up;
-        }
-        for (; w >= 0; --w) {
-          row[w] = bits;
-          bits = 0;
-        }
-        if (depth > 0) pos = static_cast<int>(i64min(static_cast<int64_t>(pos) + depth, 0x7fffffff));
+      if (par != nullptr) {
+        par += cu[s];
+        cur = i;
+        pos = clen[s];
       }
-      a.positions[t] = pos;
     }
+    a.slots[t] = slot;
+    if (a.mask != nullptr) {
+      // ancestors come in descending order, so the words are finished one by one from the last
+      uint32_t* row = a.mask + static_cast<size_t>(t) * a.mask_words;
+      int w = a.mask_words - 1, depth = -1;
+      uint32_t bits = 0;
+      while (cur >= 0) {
+        ++depth;
+        const int cw = cur >> 5;
+        if (cw >= a.mask_words) {
+          bad = true;
+        } else {
+          for (; w > cw; --w) {
+            row[w] = bits;
+            bits = 0;
+          }
+          bits |= 1u << (cur & 31);
+        }
+        const int up = __ldg(par + cur);
+        if (up >= cur || up < -1) {
+          bad = true;
+          break;
+        }
+        cur = up;
+      }
+      for (; w >= 0; --w) {
+        row[w] = bits;
+        bits = 0;
+      }
+      if (depth > 0) pos = static_cast<int>(i64min(static_cast<int64_t>(pos) + depth, 0x7fffffff));
+    }
+    a.positions[t] = pos;
   }
   if (bad) set_status(a.status, STEM_ERR_BAD_INPUT_CODE);
   if (out_of_pages) set_status(a.status, STEM_ERR_OUT_OF_PAGES_CODE);

@@ -740,6 +740,6 @@ const char* stem_status_string(stem_status_t status) {
   return "unknown status";
 }
 
-int32_t stem_version(void) { return 100; }
+int32_t stem_version(void) { return 200; }
 
 }  // extern "C"
