@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kExtendThreads, 1) cache_extend_kernel(const E
   const int tid = threadIdx.x;
   bool bad = false, out_of_pages = false;
 
-  const int cur_in = __ldg(a.cursor);
+  const int cur_in = *a.cursor;  // (may be written below, after every CTA has read it)
   const int cursor = min(max(cur_in, 0), a.num_free);
   bad |= cursor != cur_in;
   const int avail = a.num_free - cursor;

@@ -569,6 +569,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
 #pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t rr[32];
+          __syncwarp();
           tmem_ld32(o_tmem + ch * 32, rr);
           tmem_ld_wait();
           if (odd_v && valid) {
@@ -593,8 +594,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
               }
             }
           }
-          if (!valid) continue;
-          if (wk.whole) {
+          if (valid && wk.whole) {
             uint8_t* dst = static_cast<uint8_t*>(a.out) + ((tok * a.hq + hq) * static_cast<size_t>(kHeadDim) + ch * 32) * 2;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
                                    __uint_as_float(rr[q * 8 + 2 * e + 1]) * inv);
               reinterpret_cast<uint4*>(dst)[q] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          } else {
+          } else if (valid) {
             // dim by dim, so that a warp's 32 rows are one line
             float* dst = a.part_o + (part * kHeadDim + ch * 32) * a.part_rows + row;
 #pragma unroll
@@ -805,8 +805,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_dims_kernel(const _
     for (int k = warp; k < n; k += kJoinWarps) {
       if (valid) {
         const float2 ml = a.part_ml[part(pc.k0 + k) * a.part_rows + row];
-        const float w = exp2f(ml.x - m_use);  // 0 for a piece without a key that the row sees
-        sm_w[k][lane] = w;
+        const float w = exp2f(ml.x - m_use);
+        sm_w[k][lane] = ml.x == ninf ? -1.f : w;  // below 0: the row sees no key of the piece
         l += w * ml.y;
       }
     }
@@ -826,7 +826,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_dims_kernel(const _
 #pragma unroll
         for (int e = 0; e < kCols; ++e) {
           const float x = src[static_cast<size_t>(e) * a.part_rows];
-          if (w != 0.f) o[e] += w * x;  // (a piece of weight 0 may hold anything)
+          if (!(w < 0.f)) o[e] += w * x;
         }
       }
     }
