@@ -14,7 +14,7 @@ namespace {
 // Keys and queries of one sequence, as the call sees them.
 struct SeqShape {
   int tok0, n, rows;  // first packed token, new tokens, tokens that are computed
-  int ctx, kv;        // keys before the new tokens (negative when some are not cached), end of the keys
+  int ctx, kv;        // keys before the new tokens (negative when some are not cached), end of the keys; ctx <= kv
   int units;          // 0: nothing to do
   bool bad;
 };
@@ -28,8 +28,9 @@ __device__ __forceinline__ SeqShape seq_shape(const TreeArgs& a, int s) {
   r.tok0 = t0;
   r.n = r.bad ? 0 : t1 - t0;
   r.rows = min(r.n, a.max_seq_tokens);
-  r.ctx = kv - r.n;
   r.kv = kv < cap ? kv : static_cast<int>(cap);
+  // (where the table's row ends before the new tokens, no key is one of them: the last unit is then an edge, too)
+  r.ctx = min(kv - r.n, r.kv);
   r.units = r.n == 0 ? 0 : max((r.kv + a.unit_keys - 1) / a.unit_keys, 1);
   if (r.n > 0) r.bad |= r.rows < r.n || kv > cap || __ldg(a.kv_lens + s) < 0;
   return r;

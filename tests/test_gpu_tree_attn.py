@@ -433,3 +433,28 @@ def test_pages_past_32_bit_offsets():
     small = [p[pages[0].long()].contiguous() for p in pool]
     o2, l2, _ = b.stem_tree_attn(tree, b.paged_kv(*small, torch.tensor([[0, 1, 2]], **i32), 64))
     assert torch.equal(out, o2) and torch.equal(lse, l2) and torch.isfinite(out.float()).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("width,over", [(1, 1000), (3, 1000), (3, 2), (4, 77), (5, 10 ** 9)])
+def test_keys_past_the_tables_row_are_not_seen(width, over, n, fp8):
+    """kv_lens past what the table's row holds: the queries see the keys that are there and no others."""
+    c = Case([n], [width * 64 - n], 4, 2, fp8, seed=width)
+    c.table, held = np.ascontiguousarray(c.table[:, :width]), width * 64
+    assert c.kv == [held]
+    k, v = (c.f64(x.view(-1, 2, 128)[c.rows(0)], sc) for x, sc in ((c.k, c.ks), (c.v, c.vs)))
+    ctx = held + over - n
+    # as the oracle's batch: the keys that every query sees, then the new tokens that are there
+    fresh = max(held - ctx, 0)
+    j = np.arange(n)
+    mask = ((j[None, :] <= j[:, None]) & (j[None, :] < fresh)).astype(np.uint64) << (j % 32).astype(np.uint64)
+    words = np.stack([mask[:, w * 32:w * 32 + 32].sum(1) for w in range(-(-n // 32))], 1).astype(np.uint32)
+    seen = min(ctx, held)
+    pad = lambda x: np.concatenate([x, np.zeros((n - fresh, 2, 128))])  # noqa: E731
+    c.oracle = lambda: C.tree_attn(c.f64(c.q, c.qs), [pad(k)], [pad(v)], [0, n], [seen + n], words)
+    c.kv[0] = held + over
+    out, lse, st = c.gpu()
+    assert st == 8
+    got, c.kv[0], c.gpu = (out, lse, st), held, lambda: got  # bounds for the keys that exist
+    c.check(status=8)
