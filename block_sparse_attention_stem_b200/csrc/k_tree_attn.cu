@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           const uint8_t* src = sm.v[slot] + from;
           uint8_t* dst = sm.wide[h & 1];
           const bool check = (u + 1) * kUnit > wk.q.ctx;
-          const int end = wk.q.kv - u * kUnit;  // rows from here on are behind the keys
+          const int fresh = wk.q.ctx - u * kUnit;  // rows from here on are new tokens, or
+          const int end = wk.q.kv - u * kUnit;     // from here on behind the keys
           bool odd = false;
 #pragma unroll 1
           for (int step = 0; step < kUnit * 128; step += Cfg::kWidenWarps * 4 * 128) {
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) widen_e4m3x4(in[e], w[2 * e], w[2 * e + 1]);
-            if (check) {
+            if (check && r + step / 128 >= fresh) {  // a cached key's NaN is everyone's
               const bool behind = r + step / 128 >= end;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {

@@ -458,3 +458,17 @@ def test_keys_past_the_tables_row_are_not_seen(width, over, n, fp8):
     assert st == 8
     got, c.kv[0], c.gpu = (out, lse, st), held, lambda: got  # bounds for the keys that exist
     c.check(status=8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("key", [10, 63, 64, 70, 99])
+def test_a_nan_in_a_cached_value_is_everyones_wherever_it_lies(key, n, fp8):
+    """Also in the unit of keys that the new tokens begin in, in both kernels."""
+    c = Case([n], [100], 4, 2, fp8, tree=True, seed=key)
+    want, wl, _ = c.gpu()
+    c.v.view(-1, 2, 128)[c.rows(0)[key], 1, 9] = 0x7F if fp8 else float("nan")
+    out, lse, st = c.gpu()
+    assert st == 0 and torch.isnan(out[:, 2:, 9]).all()
+    out[:, 2:, 9] = want[:, 2:, 9]
+    assert torch.equal(out, want) and torch.equal(lse, wl)  # and nothing else is touched
