@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
       const int x = ((st.u - st.w.ub) & 15) * 2;
       if (x == 0) {
         // halves behind the last key read zeros, not memory
-        const int key = st.u * kUnit + lane * 64;
-        st.rows = key < st.w.q.kv ? pool_row(a, st.w.s, key) : a.num_pages * a.page_size;
+        const int key0 = st.u * kUnit;  // (a key behind the last one may not fit 32 bits)
+        st.rows = lane * 64 < st.w.q.kv - key0 ? pool_row(a, st.w.s, key0 + lane * 64) : a.num_pages * a.page_size;
       }
       const int row0 = __shfl_sync(0xffffffffu, st.rows, x), row1 = __shfl_sync(0xffffffffu, st.rows, x + 1);
       bool good = true;

@@ -472,3 +472,29 @@ def test_a_nan_in_a_cached_value_is_everyones_wherever_it_lies(key, n, fp8):
     assert st == 0 and torch.isnan(out[:, 2:, 9]).all()
     out[:, 2:, 9] = want[:, 2:, 9]
     assert torch.equal(out, want) and torch.equal(lse, wl)  # and nothing else is touched
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_largest_length(fp8):
+    """2^31 - 128 keys, sixteen pages over and over: the look-ahead over the pages stays inside the table's row.
+    An SM's accumulators take at most 2^31 / 148 / 16 = 2^19.8 products of 16 keys, each rounding cut off at
+    2^-23; a thread's sum 2^31 / 148 / 128 = 2^16.8 weights, rounded to 2^-24."""
+    P, L, hq = 16, 2 ** 31 - 128, 4
+    g = torch.Generator("cuda").manual_seed(33)
+    sc = [torch.full((h,), 0.01, device="cuda") for h in (hq, 1, 1)] if fp8 else [None] * 3
+    x = [torch.randn(n, h, 128, generator=g, device="cuda") for n, h in ((1, hq), (P * 64, 1), (P * 64, 1))]
+    enc = [(y / 0.01).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else y.to(torch.bfloat16) for y in x]
+    dec = [y.view(torch.float8_e4m3fn).double() * float(s[0]) if fp8 else y.double() for y, s in zip(enc, sc)]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.arange(L // 64, **i32).remainder(P)[None].contiguous()
+    times = torch.bincount(table[0], minlength=P).double().repeat_interleave(64)  # that each key occurs
+    tree = b.make_tree(enc[0], torch.tensor([0, 1], **i32), torch.tensor([L], **i32), 1, max_seq_tokens=1,
+                       q_scale=sc[0], k_scale=sc[1], v_scale=sc[2])
+    out, lse, ws = b.stem_tree_attn(tree, b.paged_kv(*(y.view(P, 64, 1, 128) for y in enc[1:]), table, 64))
+    assert b.stem_read_device_status(ws) == 0
+    s = dec[0][0] @ dec[1][:, 0].T / 128 ** 0.5 + times.log()
+    z = torch.logsumexp(s, 1)
+    p = torch.exp(s - z[:, None])
+    o, av = p @ dec[2][:, 0], p @ dec[2][:, 0].abs()
+    assert torch.all((out[0].double() - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** (19.8 - 23) + 2.0 ** (16.8 - 24)) * av)
+    assert torch.all((lse[:, 0].double() - z).abs() <= 2.0 ** (16.9 - 24))
