@@ -14,8 +14,17 @@
 //
 // Columns are cheap, so P is kept to more bits as several terms in columns of
 // their own, added in the epilogue.  bf16: two (cut off below p, and the rest).
-// e4m3: three, each the e4m3 of what is left, times 16 and 256 (2^-12 p in
-// all), so V is used as it is and never widened.
+// e4m3: three, each the e4m3 of what is left, times 16 and 256, so V is used as
+// it is and never widened.  With the largest weight at 2^5 that is 2^-12 p from
+// 2^-6 on and 2^-18 below, too little for the many small weights beside an
+// attention sink, so weights below 2^-8 go to three columns of their own, times
+// 2^16: a weight is off by 2^-10 of itself at most down to 2^-29 of the row's
+// largest (20 nats), and by 2^-39 of the largest below.  The second bank costs
+// zeros (six byte stores per weight instead of three): none of it shows with 8
+// rows (64 tokens over 1 to 8K keys 107.6 us with one bank or two), up to 9% with
+// 16, where P takes the place of one K buffer: three tokens over 64K 38.2 against
+// 35.0 us, sixteen 4-token trees over 16K 109 against 112 (in the 128-row kernel
+// 60.9 and 125.9).
 //
 // No reduction across the keys while the reference holds: a thread keeps its
 // key's share of every row's sum, and a value that passes the reference by more
@@ -46,35 +55,41 @@ constexpr int kThreads = 192;
 constexpr int kProducer = 4, kMmaIssuer = 5;
 constexpr int kN = 16;  // query rows at most
 constexpr int kQBufs = 2;
+// e4m3 weights below kSmall go to a bank of terms of their own, times kUp
+constexpr float kSmall = 0.00390625f, kUp = 65536.f;
 
-template <bool kFp8>
+// kRows: query rows at most
+template <bool kFp8, int kRows>
 struct NarrowCfg {
   static constexpr int kElt = kFp8 ? 1 : 2;
   static constexpr int kSlabs = kFp8 ? 1 : 2;          // 128-byte slabs of a head row
   static constexpr int kUnitBytes = kUnit * kHeadDim * kElt;
-  static constexpr int kTerms = kFp8 ? 3 : 2;          // columns per row of P^T
+  static constexpr int kTerms = kFp8 ? 6 : 2;          // columns per row of P^T
+  static constexpr int kPCols = kTerms * kRows;
   static constexpr int kStepKeys = kFp8 ? 32 : 16;     // keys per MMA of O^T
-  static constexpr int kSlots = 3;                     // of K, and of V
+  static constexpr int kVSlots = 3;
+  static constexpr int kKSlots = kFp8 && kRows > 8 ? 2 : 3;  // (P takes the third one's place)
   static constexpr int kCtas = kFp8 ? 2 : 1;           // per SM
   static constexpr int kQBytes = kN * kHeadDim * kElt;
-  static constexpr int kPBytes = kTerms * kN * kUnit * kElt;
+  static constexpr int kPBytes = kPCols * kUnit * kElt;
   static constexpr uint32_t kOCol = 2 * kN;            // S buffers at 0 and kN
   static constexpr uint32_t kTmemCols = 128;
   // P may reach 2^(kBias + kSlack): e4m3 ends at 448
-  static constexpr float kBias = kFp8 ? 4.f : 0.f;
-  static constexpr float kSlack = kFp8 ? 4.f : 8.f;
+  static constexpr float kBias = kFp8 ? 5.f : 0.f;
+  static constexpr float kSlack = kFp8 ? 3.75f : 8.f;
+  static_assert(kPCols % 16 == 0 && kOCol + kPCols <= kTmemCols && kPBytes % 1024 == 0 && kPBytes >= kRows * kUnit * 4);
 };
 
-template <bool kFp8>
+template <bool kFp8, int kRows>
 struct NarrowSmem {
-  using C = NarrowCfg<kFp8>;
-  uint8_t k[C::kSlots][C::kUnitBytes];  // 1024-aligned
-  uint8_t v[C::kSlots][C::kUnitBytes];
+  using C = NarrowCfg<kFp8, kRows>;
+  uint8_t k[C::kKSlots][C::kUnitBytes];  // 1024-aligned
+  uint8_t v[C::kVSlots][C::kUnitBytes];
   uint8_t q[kQBufs][C::kQBytes];
   uint8_t p[2][C::kPBytes];
   uint64_t q_full[kQBufs], q_empty[kQBufs];
-  uint64_t k_full[C::kSlots], k_empty[C::kSlots];
-  uint64_t v_full[C::kSlots], v_empty[C::kSlots];
+  uint64_t k_full[C::kKSlots], k_empty[C::kKSlots];
+  uint64_t v_full[C::kVSlots], v_empty[C::kVSlots];
   uint64_t s_full[2];   // S^T_h complete
   uint64_t p_full[2];   // P^T_h stored (and O scaled)
   uint64_t pv_done[2];  // O += V^T_h P^T_h complete
@@ -86,6 +101,12 @@ struct NarrowSmem {
   int odd_v[4];  // [item % 4]: item + 1 when a non-finite element of V was zeroed in it
 };
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -128,12 +149,13 @@ __device__ __forceinline__ float2 from_e4m3x2(uint16_t v) {
 
 }  // namespace
 
-template <bool kFp8>
-__global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
+template <bool kFp8, int kRows>
+__global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8, kRows>::kCtas)
     tree_narrow_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeArgs a) {
-  using Cfg = NarrowCfg<kFp8>;
+  using Cfg = NarrowCfg<kFp8, kRows>;
+  using Smem = NarrowSmem<kFp8, kRows>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  NarrowSmem<kFp8>& sm = *reinterpret_cast<NarrowSmem<kFp8>*>(smem_raw);
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const int warp = warp_id(), lane = lane_id();
 
   if (threadIdx.x == 0) {
@@ -143,8 +165,8 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
     for (int x = 0; x < 4; ++x) sm.odd_v[x] = 0;
   }
   // the barriers, a lane each, and the tensor maps' fetch, before earlier kernels are waited for
-  constexpr int kBars = 2 * kQBufs + 4 * Cfg::kSlots + 7;
-  static_assert(offsetof(NarrowSmem<kFp8>, drain) == offsetof(NarrowSmem<kFp8>, q_full) + (kBars - 1) * 8, "barriers in a row");
+  constexpr int kBars = 2 * kQBufs + 2 * Cfg::kKSlots + 2 * Cfg::kVSlots + 7;
+  static_assert(offsetof(Smem, drain) == offsetof(Smem, q_full) + (kBars - 1) * 8, "barriers in a row");
   if (warp == kMmaIssuer && lane < kBars) {
     uint64_t* bar = &sm.q_full[0] + lane;
     mbar_init(bar, bar == &sm.p_full[0] || bar == &sm.p_full[1] ? 4 : 1);
@@ -177,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
     // units before V: while V_h is the next V, the products up to S_{h+1} can
     // complete, and the Q tile of K_{h+ahead-1} may have to wait for
     // S_{h+ahead-1-kQBufs} (items of one unit): ahead <= 2 + kQBufs.
-    constexpr int kAhead = Cfg::kSlots < 2 + kQBufs ? Cfg::kSlots : 2 + kQBufs;
+    constexpr int kAhead = Cfg::kKSlots < 2 + kQBufs ? Cfg::kKSlots : 2 + kQBufs;
     struct Stream {
       Walk w;
       int u, rows, h, slot, round;
@@ -236,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
         if (!__shfl_sync(0xffffffffu, good, 0)) return false;
         ++item;
       }
-      if (!load(ks, &maps.k_pool, sm.k[0], sm.k_full, sm.k_empty, Cfg::kSlots)) return false;
+      if (!load(ks, &maps.k_pool, sm.k[0], sm.k_full, sm.k_empty, Cfg::kKSlots)) return false;
       if (ks.u == ks.w.ue) enter(ks);
       return true;
     };
@@ -246,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
     }
     for (int x = 0; x < kAhead && ok && ks.more; ++x) ok = load_k();
     while (ok && vs.more) {
-      ok = load(vs, &maps.v_pool, sm.v[0], sm.v_full, sm.v_empty, Cfg::kSlots);
+      ok = load(vs, &maps.v_pool, sm.v[0], sm.v_full, sm.v_empty, Cfg::kVSlots);
       if (ok && vs.u == vs.w.ue) enter(vs);
       if (ok && ks.more) ok = load_k();
     }
@@ -259,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
           mbar_wait_quiesce(&full[x], (last / slots) & 1, status);
         }
       };
-      quiesce(sm.k_full, Cfg::kSlots, ks.h);
-      quiesce(sm.v_full, Cfg::kSlots, vs.h);
+      quiesce(sm.k_full, Cfg::kKSlots, ks.h);
+      quiesce(sm.v_full, Cfg::kVSlots, vs.h);
       quiesce(sm.q_full, kQBufs, item);
     }
     __syncwarp();
@@ -269,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
     if (elect_one()) {
       const uint32_t fmt = kFp8 ? 0u : 1u;  // e4m3 (kind::f8f6f4) or bf16 (kind::f16)
       const uint32_t idesc_s = make_idesc(fmt, 0u, 128u, static_cast<uint32_t>(kN));
-      const uint32_t idesc_o = make_idesc(fmt, 0u, 128u, static_cast<uint32_t>(Cfg::kTerms * kN)) | (1u << 15);  // A MN-major
+      const uint32_t idesc_o = make_idesc(fmt, 0u, 128u, static_cast<uint32_t>(Cfg::kPCols)) | (1u << 15);  // A MN-major
       const uint32_t o_tmem = tmem + Cfg::kOCol;
       // two walks: S runs two units ahead of O
       Walk ws = wk;
@@ -281,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
           ++qitem;
           if (!mbar_wait(&sm.q_full[qitem % kQBufs], (qitem / kQBufs) & 1, abort, status)) return false;
         }
-        const int slot = hs % Cfg::kSlots;
-        if (!mbar_wait(&sm.k_full[slot], (hs / Cfg::kSlots) & 1, abort, status)) return false;
+        const int slot = hs % Cfg::kKSlots;
+        if (!mbar_wait(&sm.k_full[slot], (hs / Cfg::kKSlots) & 1, abort, status)) return false;
         tc_fence_after();
         // descriptors count 16-byte units
         const uint64_t dq = make_sdesc_sw128(smem_u32(sm.q[qitem % kQBufs]), 16, 1024);
@@ -313,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
       int h = 0;
       while (ok && wk.next(a, 0)) {
         for (int u = wk.ub; u < wk.ue && ok; ++u, ++h) {
-          const int slot = h % Cfg::kSlots;
+          const int slot = h % Cfg::kVSlots;
           ok = mbar_wait(&sm.p_full[h & 1], (h >> 1) & 1, abort, status) &&
-               mbar_wait(&sm.v_full[slot], (h / Cfg::kSlots) & 1, abort, status);
+               mbar_wait(&sm.v_full[slot], (h / Cfg::kVSlots) & 1, abort, status);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dv = make_sdesc_sw128(smem_u32(sm.v[slot]), kUnit * 128, 1024);
@@ -329,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)  // 16 keys per step
               if (kk < steps)
-                mma_bf16_ss(o_tmem, dv + kk * 128, dp + (kk >> 2) * (Cfg::kTerms * kN * 8) + (kk & 3) * 2, idesc_o,
+                mma_bf16_ss(o_tmem, dv + kk * 128, dp + (kk >> 2) * (Cfg::kPCols * 8) + (kk & 3) * 2, idesc_o,
                             u != wk.ub || kk != 0);
           }
           mma_commit(&sm.v_empty[slot]);
@@ -350,25 +372,25 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
     // where this key's values go in a row of P^T (row r: 128 r bytes further, chunk ^ r % 8)
     const uint32_t pchunk = kFp8 ? static_cast<uint32_t>(kx >> 4) << 4 : static_cast<uint32_t>((kx & 63) >> 3) << 4;
     const uint32_t pbyte = kFp8 ? static_cast<uint32_t>(kx & 15)
-                                : static_cast<uint32_t>(kx >> 6) * (Cfg::kTerms * kN * 128) + (kx & 7) * 2;
+                                : static_cast<uint32_t>(kx >> 6) * (Cfg::kPCols * 128) + (kx & 7) * 2;
     int h = 0;
     bool ok = !*abort;
     ok = !vote_any(!ok);
     for (int item = 0; ok && wk.next(a, 0); ++item) {
       const int rows = wk.q.rows * a.group;
       // per row: scale (e4m3: with the head's), reference less kBias, this key lane's share of the sum
-      float c[kFp8 ? kN : 1], m[kN], l[kN];
+      float c[kFp8 ? kRows : 1], m[kRows], l[kRows];
       float c_lane = a.scale_log2;  // row `lane`'s scale
       if constexpr (kFp8) {
         if (lane < rows)
           c_lane *= __ldg(a.q_scale + wk.hk_cur * a.group + lane % a.group) * __ldg(a.k_scale + wk.hk_cur);
 #pragma unroll
-        for (int r = 0; r < kN; ++r) c[r] = __shfl_sync(0xffffffffu, c_lane, r);
+        for (int r = 0; r < kRows; ++r) c[r] = __shfl_sync(0xffffffffu, c_lane, r);
       } else {
         c[0] = c_lane;
       }
 #pragma unroll
-      for (int r = 0; r < kN; ++r) m[r] = l[r] = 0.f;
+      for (int r = 0; r < kRows; ++r) m[r] = l[r] = 0.f;
       float ref = 0.f;   // row `lane`: the same as m[lane]
       bool set = false;  // row `lane` has a reference
 #pragma unroll 1
@@ -379,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
         const int key = u * kUnit + kx;
         if (edge) {
           // no NaN or infinity of V may meet a weight of zero
-          const int slot = h % Cfg::kSlots;
-          good = good && mbar_wait(&sm.v_full[slot], (h / Cfg::kSlots) & 1, abort, status);
+          const int slot = h % Cfg::kVSlots;
+          good = good && mbar_wait(&sm.v_full[slot], (h / Cfg::kVSlots) & 1, abort, status);
           if (good) {
             const int r0 = max(wk.q.ctx - u * kUnit, 0), r1 = Cfg::kStepKeys * key_steps<kUnit, Cfg::kStepKeys>(wk.q.kv, u);
             bool odd = false;
@@ -414,9 +436,9 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
         }
         __syncwarp();
         tc_fence_after();
-        uint32_t s[kN];
-#pragma unroll
-        for (int x = 0; x < kN; x += 16) tmem_ld16(tmem + kN * b + lane_off + x, s + x);
+        uint32_t s[kRows];
+        if constexpr (kRows == 8) tmem_ld8(tmem + kN * b + lane_off, s);
+        else tmem_ld16(tmem + kN * b + lane_off, s);
         tmem_ld_wait();
         uint32_t see = 0xffffffffu;  // rows that see this key
         if (edge) {
@@ -432,13 +454,13 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
             }
           }
 #pragma unroll
-          for (int r = 0; r < kN; ++r)
+          for (int r = 0; r < kRows; ++r)
             if (!((see >> r) & 1u)) s[r] = 0xff800000u;  // -inf
         }
         // t = s c - m; does a row pass its reference by more than the slack?
-        float t[kN], top = ninf;
+        float t[kRows], top = ninf;
 #pragma unroll
-        for (int r = 0; r < kN; r += 4) {
+        for (int r = 0; r < kRows; r += 4) {
           if (r < rows) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -488,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
             tc_fence_after();
             if (fine) {
 #pragma unroll 1
-              for (int n = 0; n < Cfg::kTerms * kN; ++n) {
-                const float f = __shfl_sync(0xffffffffu, alpha, n % kN);
+              for (int n = 0; n < Cfg::kPCols; ++n) {
+                const float f = __shfl_sync(0xffffffffu, alpha, n % kRows);
                 uint32_t o;
                 asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o) : "r"(o_tmem + n));
                 tmem_ld_wait();
@@ -500,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
             }
           }
 #pragma unroll
-          for (int r = 0; r < kN; ++r) {
+          for (int r = 0; r < kRows; ++r) {
             if (r < rows) {
               m[r] = __shfl_sync(0xffffffffu, ref, r);
               l[r] *= __shfl_sync(0xffffffffu, alpha, r);
@@ -515,19 +537,26 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
         // ---- weights, their share of the sums, and their terms to SMEM
         uint8_t* prow = sm.p[b] + pbyte;
 #pragma unroll
-        for (int r = 0; r < kN; r += 2) {
+        for (int r = 0; r < kRows; r += 2) {
           if (r < rows) {
             const float2 p = make_float2(fast_exp2(t[r]), r + 1 < rows ? fast_exp2(t[r + 1]) : 0.f);
             l[r] += p.x;
             l[r + 1] += p.y;
             auto at = [&](int n) -> uint8_t* { return prow + n * 128 + (pchunk ^ ((n & 7) << 4)); };
             if constexpr (kFp8) {
-              float2 left = p;
+              // three terms in one of two banks of columns, zeros in the other
+              constexpr int kTerm = kRows * 128, kBank = 3 * kTerm;  // bytes
+              const bool s0 = p.x < kSmall, s1 = p.y < kSmall;
+              uint8_t *in0 = at(r) + (s0 ? kBank : 0), *no0 = at(r) + (s0 ? 0 : kBank);
+              uint8_t *in1 = at(r + 1) + (s1 ? kBank : 0), *no1 = at(r + 1) + (s1 ? 0 : kBank);
+              float2 left = fmul2(p, make_float2(s0 ? kUp : 1.f, s1 ? kUp : 1.f));
 #pragma unroll
               for (int e = 0; e < 3; ++e) {
                 const uint16_t w = to_e4m3x2(left.x, left.y);
-                *at(e * kN + r) = static_cast<uint8_t>(w);
-                *at(e * kN + r + 1) = static_cast<uint8_t>(w >> 8);
+                in0[e * kTerm] = static_cast<uint8_t>(w);
+                in1[e * kTerm] = static_cast<uint8_t>(w >> 8);
+                no0[e * kTerm] = 0;
+                no1[e * kTerm] = 0;
                 if (e < 2) left = fmul2(fsub2(left, from_e4m3x2(w)), make_float2(16.f, 16.f));
               }
             } else {
@@ -539,8 +568,8 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
               const uint32_t lo = pack_bf16x2(p.x - __uint_as_float(e0), p.y - __uint_as_float(e1));
               *reinterpret_cast<uint16_t*>(at(r)) = static_cast<uint16_t>(e0 >> 16);
               *reinterpret_cast<uint16_t*>(at(r + 1)) = static_cast<uint16_t>(e1 >> 16);
-              *reinterpret_cast<uint16_t*>(at(kN + r)) = static_cast<uint16_t>(lo);
-              *reinterpret_cast<uint16_t*>(at(kN + r + 1)) = static_cast<uint16_t>(lo >> 16);
+              *reinterpret_cast<uint16_t*>(at(kRows + r)) = static_cast<uint16_t>(lo);
+              *reinterpret_cast<uint16_t*>(at(kRows + r + 1)) = static_cast<uint16_t>(lo >> 16);
             }
           }
         }
@@ -562,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
       // done), then one warp adds the 128 of a row
       float* share = reinterpret_cast<float*>(sm.p[0]);
 #pragma unroll
-      for (int r = 0; r < kN; ++r)
+      for (int r = 0; r < kRows; ++r)
         if (r < rows) share[r * 128 + kx] = l[r];
       vote_any(false);
 #pragma unroll 1
@@ -583,11 +612,12 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
         uint32_t o[Cfg::kTerms];
 #pragma unroll
         for (int e = 0; e < Cfg::kTerms; ++e)
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o[e]) : "r"(o_tmem + e * kN + r));
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(o[e]) : "r"(o_tmem + e * kRows + r));
         tmem_ld_wait();
         float acc = __uint_as_float(o[0]);
         if constexpr (kFp8)
-          acc += __uint_as_float(o[1]) * 0.0625f + __uint_as_float(o[2]) * 0.00390625f;
+          acc += __uint_as_float(o[1]) * 0.0625f + __uint_as_float(o[2]) * 0.00390625f +
+                 (__uint_as_float(o[3]) + __uint_as_float(o[4]) * 0.0625f + __uint_as_float(o[5]) * 0.00390625f) * (1.f / kUp);
         else
           acc += __uint_as_float(o[1]);
         if (odd_v) {
@@ -641,18 +671,19 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8>::kCtas)
   }
 }
 
-template <bool kFp8>
+template <bool kFp8, int kRows>
 static cudaError_t launch_narrow_t(const TreeMaps& maps, const TreeArgs& args, cudaStream_t stream) {
-  const size_t smem = sizeof(NarrowSmem<kFp8>);
-  static_assert(sizeof(NarrowSmem<kFp8>) <= (kFp8 ? 115712 : 232448), "CTAs per SM");
+  const size_t smem = sizeof(NarrowSmem<kFp8, kRows>);
+  static_assert(sizeof(NarrowSmem<kFp8, kRows>) <= (kFp8 ? 115712 : 232448), "CTAs per SM");
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(tree_narrow_kernel<kFp8>), smem, allowed);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(tree_narrow_kernel<kFp8, kRows>), smem, allowed);
   if (e != cudaSuccess) return e;
-  return launch_after(tree_narrow_kernel<kFp8>, dim3(args.ranges), kThreads, smem, stream, maps, args);
+  return launch_after(tree_narrow_kernel<kFp8, kRows>, dim3(args.ranges), kThreads, smem, stream, maps, args);
 }
 
 cudaError_t launch_tree_narrow(const TreeMaps& maps, const TreeArgs& args, bool fp8, cudaStream_t stream) {
-  return fp8 ? launch_narrow_t<true>(maps, args, stream) : launch_narrow_t<false>(maps, args, stream);
+  if (!fp8) return launch_narrow_t<false, 16>(maps, args, stream);
+  return args.box_rows <= 8 ? launch_narrow_t<true, 8>(maps, args, stream) : launch_narrow_t<true, 16>(maps, args, stream);
 }
 
 }  // namespace stem

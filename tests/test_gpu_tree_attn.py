@@ -498,3 +498,47 @@ def test_the_largest_length(fp8):
     o, av = p @ dec[2][:, 0], p @ dec[2][:, 0].abs()
     assert torch.all((out[0].double() - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** (19.8 - 23) + 2.0 ** (16.8 - 24)) * av)
     assert torch.all((lse[:, 0].double() - z).abs() <= 2.0 ** (16.9 - 24))
+
+
+def attention_sink(n, ctx, nats, fp8, where, ones, seed=0):
+    """One key `nats` above all others, with a value of zero: the output is what the others' weights leave."""
+    c = Case([n], [ctx], 4, 1, fp8, seed=seed, scale=float(nats) if nats else 1.0)
+    one, rows = (0x38 if fp8 else 1.0), c.rows(0)
+    if fp8:
+        c.qs, c.ks, c.vs = (torch.ones(h, device="cuda") for h in (4, 1, 1))
+    for x, at in ((c.q, slice(None)), (c.k.view(-1, 1, 128), rows)):
+        x[at] = 0
+    c.q[..., 0] = one
+    v = torch.randn(len(rows), 1, 128, generator=torch.Generator("cuda").manual_seed(seed), device="cuda")
+    v = c._enc(torch.ones_like(v) if ones else v, c.vs)
+    v[where] = 0
+    c.v.view(-1, 1, 128)[rows] = v
+    if nats:
+        c.k.view(-1, 1, 128)[rows[where], 0, 0] = one
+    return c
+
+
+def check_tail(n, ctx, nats, fp8, where):
+    """At 20 nats a weight is 2^-28.9 of the largest; in e4m3 it is off by at most 2^-9 of itself there, in bf16 by 2^-15."""
+    for ones in (True, False):
+        c = attention_sink(n, ctx, nats, fp8, where, ones, seed=nats)
+        out, lse, st = c.gpu()
+        assert st == 0
+        o, z, e = c.oracle()
+        out = out.double().cpu().numpy()
+        logit, L = 136 * 2.0 ** -24 * e["qk"], ctx + n
+        w = (2.0 ** -9 if fp8 else 2.0 ** -14) + 2 * logit + 2.0 ** -20 + 2 * L * 2.0 ** -24
+        tol = 2.0 ** -8 * np.abs(o) + w[..., None] * e["absav"]
+        assert np.all(np.abs(out - o) <= tol), float((np.abs(out - o) / tol).max())
+        assert np.all(np.abs(lse.double().cpu().numpy() - z) <= logit.T + L * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * np.abs(z))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("ctx,where", [(100, 0), (8192, 0), (8192, 5000)])
+@pytest.mark.parametrize("nats", [0, 6, 11, 14, 15, 16, 18, 20])
+def test_the_tail_of_the_weights(nats, ctx, where, n, fp8):
+    """Weights far below the largest keep their share (4 and 12 rows).  e4m3: three terms of e4m3, with the
+    largest weight at 2^5 or more; below 2^-8 times 2^16, so that 2^-23.9 is off by half a step of 2^-9 2^-8 2^-16 (2^-34),
+    and just above 2^-8 by 2^-18."""
+    check_tail(n, ctx, nats, fp8, where)
