@@ -542,3 +542,12 @@ def test_the_tail_of_the_weights(nats, ctx, where, n, fp8):
     largest weight at 2^5 or more; below 2^-8 times 2^16, so that 2^-23.9 is off by half a step of 2^-9 2^-8 2^-16 (2^-34),
     and just above 2^-8 by 2^-18."""
     check_tail(n, ctx, nats, fp8, where)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [5, 33])
+@pytest.mark.parametrize("ctx,where", [(100, 0), (8192, 0), (8192, 5000)])
+@pytest.mark.parametrize("nats", [0, 6, 11, 14, 15, 16, 18, 20])
+def test_the_tail_of_the_weights_in_full_tiles(nats, ctx, where, n, fp8):
+    """e4m3: f16 with the largest weight at 2^13 or more, so that 2^-15.9 is off by half a step of 2^-24."""
+    check_tail(n, ctx, nats, fp8, where)
