@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
       const int hq = wk.hk_cur * a.group + g;
       float c = a.scale_log2;
       if constexpr (kFp8) c *= __ldg(a.q_scale + hq) * __ldg(a.k_scale + wk.hk_cur);
+      c = logit_scale(c);
       float m_ref = ninf, l = 0.f;
       // the row's first mask words now, so that the item's last units do not wait for them
       uint64_t known = 0ull;

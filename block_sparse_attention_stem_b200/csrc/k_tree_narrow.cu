@@ -381,13 +381,15 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8, kRows>::kCtas)
       // per row: scale (e4m3: with the head's), reference less kBias, this key lane's share of the sum
       float c[kFp8 ? kRows : 1], m[kRows], l[kRows];
       float c_lane = a.scale_log2;  // row `lane`'s scale
-      if constexpr (kFp8) {
+      if constexpr (!kFp8) {
+        c_lane = logit_scale(c_lane);
+        c[0] = c_lane;
+      } else {
         if (lane < rows)
           c_lane *= __ldg(a.q_scale + wk.hk_cur * a.group + lane % a.group) * __ldg(a.k_scale + wk.hk_cur);
+        c_lane = logit_scale(c_lane);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) c[r] = __shfl_sync(0xffffffffu, c_lane, r);
-      } else {
-        c[0] = c_lane;
       }
 #pragma unroll
       for (int r = 0; r < kRows; ++r) m[r] = l[r] = 0.f;

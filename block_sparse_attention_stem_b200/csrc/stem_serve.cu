@@ -101,6 +101,8 @@ stem_status_t check_rows(const void* in, int64_t stride, int heads, const void* 
   return STEM_OK;
 }
 
+constexpr double kMaxScale = 0x1p127;  // times log2(e) it is still an fp32 number
+
 struct TreeLayout {
   int group, tile_tokens, box_tokens, tiles, ranges, part_rows, unit_keys;
   size_t off_cta, off_unit0, off_ml, off_o, bytes;
@@ -113,7 +115,7 @@ stem_status_t tree_layout(const stem_tree_t* t, TreeLayout* out) {
   if (t->num_q_heads < 1 || t->num_kv_heads < 1 || t->num_q_heads % t->num_kv_heads != 0) return STEM_ERR_INVALID_ARG;
   if (t->head_dim != kHeadDim) return t->head_dim < 1 ? STEM_ERR_INVALID_ARG : STEM_ERR_UNSUPPORTED;
   if (t->mask ? t->mask_words < 1 : t->mask_words < 0) return STEM_ERR_INVALID_ARG;
-  if (!(t->softmax_scale >= 0.0) || !std::isfinite(t->softmax_scale)) return STEM_ERR_INVALID_ARG;
+  if (!(t->softmax_scale >= 0.0) || t->softmax_scale > kMaxScale) return STEM_ERR_INVALID_ARG;
   if (t->total_tokens > (1 << 30) || static_cast<int64_t>(t->num_seqs) * t->num_kv_heads > (1 << 30))
     return STEM_ERR_UNSUPPORTED;
   TreeLayout l{};

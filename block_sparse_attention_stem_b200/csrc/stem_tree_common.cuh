@@ -140,6 +140,10 @@ __device__ __forceinline__ uint64_t visible(const TreeArgs& a, const SeqShape& q
   return bits;
 }
 
+// A logit's factor, at least 2^-126: hidden scores are -inf, which times zero would be NaN,
+// and with a factor this small all logits vanish anyway.
+__device__ __forceinline__ float logit_scale(float c) { return c < 1.17549435e-38f ? 1.17549435e-38f : c; }
+
 // Pool row of key u of sequence s, or the first row past the pool (reads zeros).
 __device__ __forceinline__ int pool_row(const TreeArgs& a, int s, int u) {
   const int pg = u / a.page_size;

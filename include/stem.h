@@ -480,7 +480,7 @@ typedef struct {
   const float* q_scale;       /* fp8 only, as stem_qkv_t, > 0 */
   const float* k_scale;
   const float* v_scale;
-  double softmax_scale;       /* 0 selects 1/sqrt(head_dim) */
+  double softmax_scale;       /* 0 selects 1/sqrt(head_dim); at most 2^127 */
 } stem_tree_t;
 
 /* Workspace bytes of stem_tree_attn for this description (host only; reads

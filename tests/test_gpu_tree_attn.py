@@ -551,3 +551,15 @@ def test_the_tail_of_the_weights(nats, ctx, where, n, fp8):
 def test_the_tail_of_the_weights_in_full_tiles(nats, ctx, where, n, fp8):
     """e4m3: f16 with the largest weight at 2^13 or more, so that 2^-15.9 is off by half a step of 2^-24."""
     check_tail(n, ctx, nats, fp8, where)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [5, 40])
+@pytest.mark.parametrize("scale", [1e-30, 1e-44, 1e-60])
+def test_scales_below_the_range_of_fp32(scale, n, fp8):
+    """All logits vanish: the mean over the keys that a query sees, and no others."""
+    Case([n], [70], 4, 2, fp8, tree=True, seed=n, scale=scale).check()
+    if fp8:
+        c = Case([n], [70], 4, 2, fp8, tree=True, seed=n)
+        c.qs, c.ks = torch.full_like(c.qs, scale ** 0.5), torch.full_like(c.ks, scale ** 0.5)
+        c.check()

@@ -254,3 +254,9 @@ def test_oracle_extend_of_a_small_step():
     assert r["cu"].tolist() == [0, 2, 3] and r["kv"].tolist() == [65, 65] and not r["status"]
     t = C.extend([[0, -1]], 64, 10, [3], [4], [1], [], 0, 4, parents=[-1, 0, 0, 1], mask_words=1)
     assert t["mask"][:, 0].tolist() == [0b1, 0b11, 0b101, 0b1011] and t["positions"].tolist() == [3, 4, 4, 5]
+
+
+@pytest.mark.parametrize("scale,code", [(1e-300, OK), (2.0 ** 127, OK), (2.0 ** 127 * 1.001, INVALID), (1e300, INVALID),
+                                        (math.inf, INVALID)])
+def test_tree_plan_refuses_scales_past_fp32(scale, code):
+    assert plan(tree(softmax_scale=scale))[0] == code
