@@ -213,6 +213,23 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _elsewhere(stream, device, fn, *args):
+    """fn(*args) with `stream` current, as every call with stream= runs.  What it
+    makes then belongs to that stream: the allocator does not hand it to work on
+    another one, and does not take it from work that another one still has to do.
+    Results may be used on the caller's current stream too."""
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        made = fn(*args)
+    if here != stream:
+        for t in made if isinstance(made, tuple) else vars(made).values():
+            if t is not None:
+                t.record_stream(here)
+    return made
+
+
 def _ws(nbytes: int, device, ws):
     if ws is None:
         ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -220,6 +237,8 @@ def _ws(nbytes: int, device, ws):
 
 
 def stem_score(qkv: QKV, params: StemParams, scores=None, vbonus=None, ws=None, stream=None):
+    if stream is not None:
+        return _elsewhere(stream, qkv.q.device, stem_score, qkv, params, scores, vbonus, ws)
     pl = stem_plan(qkv, params)
     dev = qkv.q.device
     hq, hkv = qkv.q.shape[1], qkv.k.shape[1]
@@ -229,12 +248,14 @@ def stem_score(qkv: QKV, params: StemParams, scores=None, vbonus=None, ws=None, 
         vbonus = torch.empty(hkv, pl.nb_total, dtype=torch.float32, device=dev)
     ws = _ws(pl.ws_bytes, dev, ws)
     _check(LIB.stem_score(ctypes.byref(qkv.desc), ctypes.byref(params), _ptr(scores), _ptr(vbonus),
-                          _ptr(ws), ws.numel(), _stream(stream)), "stem_score")
+                          _ptr(ws), ws.numel(), _stream(None)), "stem_score")
     return scores, vbonus, ws
 
 
 def stem_select(qkv: QKV, params: StemParams, scores, budgets=None, row_ptr=None, col_idx=None, ws=None,
                 stream=None):
+    if stream is not None:
+        return _elsewhere(stream, scores.device, stem_select, qkv, params, scores, budgets, row_ptr, col_idx, ws)
     pl = stem_plan(qkv, params)
     dev = scores.device
     if budgets is None:
@@ -245,13 +266,15 @@ def stem_select(qkv: QKV, params: StemParams, scores, budgets=None, row_ptr=None
         col_idx = torch.empty(max(pl.nnz, 1), dtype=torch.int32, device=dev)
     ws = _ws(pl.ws_bytes, dev, ws)
     _check(LIB.stem_select(ctypes.byref(qkv.desc), ctypes.byref(params), _ptr(scores), _ptr(budgets),
-                           _ptr(row_ptr), _ptr(col_idx), _ptr(ws), ws.numel(), _stream(stream)), "stem_select")
+                           _ptr(row_ptr), _ptr(col_idx), _ptr(ws), ws.numel(), _stream(None)), "stem_select")
     return budgets, row_ptr, col_idx[:pl.nnz], ws
 
 
 def stem_score_select(qkv: QKV, params: StemParams, scores=None, vbonus=None, budgets=None, row_ptr=None,
                       col_idx=None, ws=None, stream=None):
     """stem_score then stem_select in one call (in one pass when params.select_mode is 1)."""
+    if stream is not None:
+        return _elsewhere(stream, qkv.q.device, stem_score_select, qkv, params, scores, vbonus, budgets, row_ptr, col_idx, ws)
     pl = stem_plan(qkv, params)
     dev = qkv.q.device
     hq, hkv = qkv.q.shape[1], qkv.k.shape[1]
@@ -266,7 +289,7 @@ def stem_score_select(qkv: QKV, params: StemParams, scores=None, vbonus=None, bu
     ws = _ws(pl.ws_bytes, dev, ws)
     _check(LIB.stem_score_select(ctypes.byref(qkv.desc), ctypes.byref(params), _ptr(scores), _ptr(vbonus),
                                  _ptr(budgets), _ptr(row_ptr), _ptr(col_idx), _ptr(ws), ws.numel(),
-                                 _stream(stream)), "stem_score_select")
+                                 _stream(None)), "stem_score_select")
     return scores, budgets, row_ptr, col_idx[:pl.nnz], ws
 
 
@@ -302,6 +325,8 @@ def paged_kv(k_pages, v_pages, page_table, page_size: int) -> PagedKV:
 
 def stem_bsa_fwd_paged(qkv: QKV, kv: PagedKV, params: StemParams, row_ptr, col_idx, out=None, lse=None,
                        ws=None, stream=None):
+    if stream is not None:
+        return _elsewhere(stream, qkv.q.device, stem_bsa_fwd_paged, qkv, kv, params, row_ptr, col_idx, out, lse, ws)
     pl = stem_plan(qkv, params)
     dev = qkv.q.device
     T, hq = qkv.total_tokens, qkv.q.shape[1]
@@ -311,12 +336,14 @@ def stem_bsa_fwd_paged(qkv: QKV, kv: PagedKV, params: StemParams, row_ptr, col_i
         lse = torch.empty(hq, T, dtype=torch.float32, device=dev)
     ws = _ws(pl.ws_bytes, dev, ws)
     _check(LIB.stem_bsa_fwd_paged(ctypes.byref(qkv.desc), ctypes.byref(kv.desc), ctypes.byref(params), _ptr(row_ptr),
-                                  _ptr(col_idx), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+                                  _ptr(col_idx), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(None)),
            "stem_bsa_fwd_paged")
     return out, lse, ws
 
 
 def stem_bsa_fwd(qkv: QKV, params: StemParams, row_ptr, col_idx, out=None, lse=None, ws=None, stream=None):
+    if stream is not None:
+        return _elsewhere(stream, qkv.q.device, stem_bsa_fwd, qkv, params, row_ptr, col_idx, out, lse, ws)
     pl = stem_plan(qkv, params)
     dev = qkv.q.device
     T, hq = qkv.total_tokens, qkv.q.shape[1]
@@ -326,12 +353,14 @@ def stem_bsa_fwd(qkv: QKV, params: StemParams, row_ptr, col_idx, out=None, lse=N
         lse = torch.empty(hq, T, dtype=torch.float32, device=dev)
     ws = _ws(pl.ws_bytes, dev, ws)
     _check(LIB.stem_bsa_fwd(ctypes.byref(qkv.desc), ctypes.byref(params), _ptr(row_ptr), _ptr(col_idx),
-                            _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "stem_bsa_fwd")
+                            _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(None)), "stem_bsa_fwd")
     return out, lse, ws
 
 
 def stem_prefill(qkv: QKV, params: StemParams, out=None, lse=None, row_ptr=None, col_idx=None, ws=None,
                  stream=None, return_lists=True):
+    if stream is not None:
+        return _elsewhere(stream, qkv.q.device, stem_prefill, qkv, params, out, lse, row_ptr, col_idx, ws, None, return_lists)
     pl = stem_plan(qkv, params)
     dev = qkv.q.device
     T, hq = qkv.total_tokens, qkv.q.shape[1]
@@ -345,7 +374,7 @@ def stem_prefill(qkv: QKV, params: StemParams, out=None, lse=None, row_ptr=None,
         col_idx = torch.empty(max(pl.nnz, 1), dtype=torch.int32, device=dev)
     ws = _ws(pl.ws_prefill_bytes, dev, ws)
     _check(LIB.stem_prefill(ctypes.byref(qkv.desc), ctypes.byref(params), _ptr(out), _ptr(lse), _ptr(row_ptr),
-                            _ptr(col_idx), _ptr(ws), ws.numel(), _stream(stream)), "stem_prefill")
+                            _ptr(col_idx), _ptr(ws), ws.numel(), _stream(None)), "stem_prefill")
     return out, lse, row_ptr, (None if col_idx is None else col_idx[:pl.nnz]), ws
 
 
@@ -354,6 +383,9 @@ def stem_prefill_host(qkv: QKV, params: StemParams, q_host, k_host, v_host, out_
     """stem_prefill with inputs and outputs in (page-locked) host tensors; the
     device tensors of `qkv` are filled by the call, transfers overlap compute.
     Only enqueues: synchronize `stream` before reading out_host / lse_host."""
+    if stream is not None:
+        return _elsewhere(stream, qkv.q.device, stem_prefill_host, qkv, params, q_host, k_host, v_host, out_host, lse_host,
+                          out, lse, ws)
     pl = stem_plan(qkv, params)
     dev = qkv.q.device
     T, hq = qkv.total_tokens, qkv.q.shape[1]
@@ -371,7 +403,7 @@ def stem_prefill_host(qkv: QKV, params: StemParams, q_host, k_host, v_host, out_
     ws = _ws(pl.ws_prefill_bytes, dev, ws)
     _check(LIB.stem_prefill_host(ctypes.byref(qkv.desc), ctypes.byref(params), _ptr(q_host), _ptr(k_host),
                                  _ptr(v_host), _ptr(out), _ptr(lse), _ptr(out_host), _ptr(lse_host), _ptr(ws),
-                                 ws.numel(), _stream(stream)), "stem_prefill_host")
+                                 ws.numel(), _stream(None)), "stem_prefill_host")
     return out, lse, ws
 
 
@@ -379,6 +411,8 @@ def stem_prefill_noalloc(qkv: QKV, params: StemParams, out=None, lse=None, row_p
                          stream=None, return_lists=True):
     """stem_prefill on the library's built-in 32 MiB workspace (for callers that
     cannot allocate one); the outputs are still the caller's."""
+    if stream is not None:
+        return _elsewhere(stream, qkv.q.device, stem_prefill_noalloc, qkv, params, out, lse, row_ptr, col_idx, None, return_lists)
     pl = stem_plan(qkv, params)
     dev = qkv.q.device
     T, hq = qkv.total_tokens, qkv.q.shape[1]
@@ -391,7 +425,7 @@ def stem_prefill_noalloc(qkv: QKV, params: StemParams, out=None, lse=None, row_p
     if return_lists and col_idx is None:
         col_idx = torch.empty(max(pl.nnz, 1), dtype=torch.int32, device=dev)
     _check(LIB.stem_prefill_noalloc(ctypes.byref(qkv.desc), ctypes.byref(params), _ptr(out), _ptr(lse),
-                                    _ptr(row_ptr), _ptr(col_idx), _stream(stream)), "stem_prefill_noalloc")
+                                    _ptr(row_ptr), _ptr(col_idx), _stream(None)), "stem_prefill_noalloc")
     return out, lse, row_ptr, (None if col_idx is None else col_idx[:pl.nnz])
 
 
@@ -407,20 +441,11 @@ def stem_noalloc_read_device_status(stream=None) -> int:
 # ------------------------------------------------------------------ the paged cache
 # These run once per layer and token: the checks are kept to a few comparisons
 # of attributes, and nothing is looked up that the descriptors already hold.
-def _on(device, stream) -> int:
-    """The stream a call runs on: the caller's, or the current one of the tensors' device."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-    return stream.cuda_stream
-
-
-def _run(device, stream, where, fn, *args):
-    """fn(*args, stream) with the tensors' device current."""
+def _run(device, where, fn, *args):
+    """fn(*args, current stream of the tensors' device) with that device current."""
     if device.type != "cuda":
         raise ValueError(f"{where}: the tensors must be on a GPU, not on {device}")
-    on = _on(device, stream)
+    on = torch._C._cuda_getCurrentRawStream(device.index)
     if torch._C._cuda_getDevice() == device.index:
         code = fn(*args, on)
     else:
@@ -460,6 +485,9 @@ def stem_cache_extend(page_table, page_size: int, num_pages: int, cache_lens, ne
     Out-of-range values and an exhausted free list are reported in the
     workspace's status word."""
     dev = page_table.device
+    if stream is not None:
+        return _elsewhere(stream, dev, stem_cache_extend, page_table, page_size, num_pages, cache_lens, new_lens, held_pages,
+                          free_pages, cursor, max_tokens, parents, mask_words, out, ws)
     i32 = torch.int32
     if page_table.dim() != 2:
         raise ValueError("page_table must be [num_seqs, max_pages]")
@@ -496,7 +524,7 @@ def stem_cache_extend(page_table, page_size: int, num_pages: int, cache_lens, ne
     desc = StemCacheStep(S, max_tokens, page_size, num_pages, page_table.shape[1], free_pages.shape[0], words,
                          cache_lens.data_ptr(), new_lens.data_ptr(), held_pages.data_ptr(), free_pages.data_ptr(),
                          cursor.data_ptr(), parents.data_ptr() if tree else None)
-    _run(dev, stream, "stem_cache_extend", LIB.stem_cache_extend, ctypes.byref(desc), page_table.data_ptr(),
+    _run(dev, "stem_cache_extend", LIB.stem_cache_extend, ctypes.byref(desc), page_table.data_ptr(),
          out.held.data_ptr(), out.cursor.data_ptr(), out.cu_seqlens.data_ptr(), out.kv_lens.data_ptr(),
          out.slots.data_ptr(), out.positions.data_ptr(), out.mask.data_ptr() if tree else None, ws.data_ptr(), ws.numel())
     return out
@@ -535,6 +563,9 @@ def stem_rope(rope: StemRope, q, k, v, positions, cache: PagedKV | None = None, 
     e4m3 bytes (uint8) when the scales, fp32 [H], are given (or `fp8` says so).
     v may be None without a cache; so may q or k."""
     dev = positions.device
+    if stream is not None:
+        return _elsewhere(stream, dev, stem_rope, rope, q, k, v, positions, cache, slots, q_scale, k_scale, v_scale, q_out,
+                          k_out, v_out, fp8)
     T = positions.shape[0] if positions.dim() else 1
     _need("positions", positions, torch.int32, (T,), dev)
     if fp8 is None:
@@ -600,7 +631,7 @@ def stem_rope(rope: StemRope, q, k, v, positions, cache: PagedKV | None = None, 
         raise ValueError("scales are for e4m3 outputs")
     io = StemRopeIO(T, hq, hkv, 128 if d is None else d, STEM_FP8_E4M3 if fp8 else STEM_BF16, positions.data_ptr(),
                     pslots, pq, pk, pv, sq, sk, sv, pqs, pks, pvs, pqo, pko, pvo)
-    _run(dev, stream, "stem_rope", LIB.stem_rope, ctypes.byref(rope), ctypes.byref(io), pcache)
+    _run(dev, "stem_rope", LIB.stem_rope, ctypes.byref(rope), ctypes.byref(io), pcache)
     return q_out, k_out, v_out
 
 
@@ -660,6 +691,8 @@ def stem_tree_attn(tree: TreeQ, kv: PagedKV, out=None, lse=None, ws=None, stream
     """Attention of a step's queries over the paged cache: out bf16 [T, Hq, 128],
     lse fp32 [Hq, T], and the workspace (whose status word tells of bad lengths)."""
     q = tree.q
+    if stream is not None:
+        return _elsewhere(stream, q.device, stem_tree_attn, tree, kv, out, lse, ws)
     desc = tree.desc
     T, hq, d = q.shape
     if kv.kind != tree.kind:
@@ -678,7 +711,7 @@ def stem_tree_attn(tree: TreeQ, kv: PagedKV, out=None, lse=None, ws=None, stream
         _need("lse", lse, torch.float32, (hq, T), dev)
     if ws is None:
         ws = _ws(stem_tree_ws_bytes(tree), dev, None)
-    _run(dev, stream, "stem_tree_attn", LIB.stem_tree_attn, ctypes.byref(desc), ctypes.byref(kv.desc), out.data_ptr(),
+    _run(dev, "stem_tree_attn", LIB.stem_tree_attn, ctypes.byref(desc), ctypes.byref(kv.desc), out.data_ptr(),
          lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse, ws
 

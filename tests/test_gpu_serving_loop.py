@@ -190,3 +190,45 @@ def test_a_decoding_step_as_one_graph():
         sv.check(o, z, q_rot, np.array([0, 1, 2]))
     assert b.stem_read_device_status(ws) == 0 and b.stem_read_device_status(out.ws) == 0
     assert held.tolist() == [3, 2] and int(cursor) == 5
+
+
+def test_outputs_of_calls_on_another_stream_belong_to_it():
+    """Memory that a call made on `stream` is not handed to the current stream when it is dropped."""
+    T, S = 300, 2
+    g = torch.Generator("cuda").manual_seed(7)
+    q, k, v = (torch.randn(T, h, 128, generator=g, device="cuda").to(torch.bfloat16) for h in (HQ, HKV, HKV))
+    qkv, params = b.make_qkv(q, k, v, [0, 130, T]), b.make_params()
+    scores, _, _ = b.stem_score(qkv, params)
+    _, rp, ci, _ = b.stem_select(qkv, params, scores)
+    pages = [torch.zeros(8, PS, HKV, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    cache = b.paged_kv(*pages, i32([[0, 1, 2, -1], [3, 4, 5, -1]]), PS)
+    tree = b.make_tree(q, i32([0, 130, T]), i32([130, T - 130]), HKV)
+    pos, table = i32(np.arange(T)), i32(np.full((S, 8), -1))
+    step = [i32(x) for x in ([0, 5], [3, 4], [0, 1], [6, 7, 8], [0])]
+    calls = [
+        lambda **kw: b.stem_score(qkv, params, **kw),
+        lambda **kw: b.stem_select(qkv, params, scores, **kw),
+        lambda **kw: b.stem_score_select(qkv, params, **kw),
+        lambda **kw: b.stem_bsa_fwd(qkv, params, rp, ci, **kw),
+        lambda **kw: b.stem_bsa_fwd_paged(qkv, cache, params, rp, ci, **kw),
+        lambda **kw: b.stem_prefill(qkv, params, **kw),
+        lambda **kw: b.stem_rope(b.make_rope(), q, k, v, pos, **kw),
+        lambda **kw: b.stem_tree_attn(tree, cache, **kw),
+        lambda **kw: vars(b.stem_cache_extend(table, PS, 64, *step, 9, **kw)).values(),
+    ]
+    for call in calls:
+        s = torch.cuda.Stream()
+        want = [t for t in call() if t is not None]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(10 ** 7)
+        got = [t for t in call(stream=s) if t is not None]
+        shapes = [(t.shape, t.dtype) for t in got]
+        places = {t.untyped_storage().data_ptr() for t in got if t.numel()}
+        s.synchronize()
+        # (the workspace, whose scratch is nobody's, is the last one)
+        assert all(torch.equal(x, y) for x, y in zip(want[:-1], got[:-1]))
+        del got
+        fresh = [torch.empty(shape, dtype=dt, device="cuda") for shape, dt in shapes for _ in range(2)]
+        assert places.isdisjoint(t.untyped_storage().data_ptr() for t in fresh)
+        del fresh

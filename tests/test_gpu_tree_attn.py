@@ -563,3 +563,24 @@ def test_scales_below_the_range_of_fp32(scale, n, fp8):
         c = Case([n], [70], 4, 2, fp8, tree=True, seed=n)
         c.qs, c.ks = torch.full_like(c.qs, scale ** 0.5), torch.full_like(c.ks, scale ** 0.5)
         c.check()
+
+
+def test_calls_on_other_streams_use_memory_of_their_own():
+    """stream=: what the call makes for itself may not be handed to a call on another stream while it is in use."""
+    c = Case([30, 7], [9000, 15000], 8, 2, tree=True, seed=27)
+    out, lse, _ = c.gpu()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got, places = [], {}
+    for s in streams:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(10 ** 7)  # some milliseconds: every call below is enqueued while it runs
+    for s in streams * 3:
+        o, z, ws = b.stem_tree_attn(c.tree, c.cache, stream=s)
+        places.setdefault(ws.data_ptr(), set()).add(s)
+        got.append((o, z))
+        del ws
+    torch.cuda.synchronize()
+    assert all(len(s) == 1 for s in places.values())
+    for o, z in got:
+        assert torch.equal(o, out) and torch.equal(z, lse)
