@@ -462,6 +462,11 @@ def _need(name, t, dtype, shape, device):
                          f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
+def _need_ws(ws, device):
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}, got strides {ws.stride()} on {ws.device}")
+
+
 @dataclass
 class CacheStep:
     """Outputs of stem_cache_extend (int32; the mask's words as int32 bit patterns)."""
@@ -520,13 +525,14 @@ def stem_cache_extend(page_table, page_size: int, num_pages: int, cache_lens, ne
             _need("out.mask", out.mask, i32, (max_tokens, words), dev)
     if ws is None:
         ws = out.ws if out.ws is not None else _ws(256, dev, None)
+    _need_ws(ws, dev)
     out.ws = ws
     desc = StemCacheStep(S, max_tokens, page_size, num_pages, page_table.shape[1], free_pages.shape[0], words,
                          cache_lens.data_ptr(), new_lens.data_ptr(), held_pages.data_ptr(), free_pages.data_ptr(),
                          cursor.data_ptr(), parents.data_ptr() if tree else None)
     _run(dev, "stem_cache_extend", LIB.stem_cache_extend, ctypes.byref(desc), page_table.data_ptr(),
          out.held.data_ptr(), out.cursor.data_ptr(), out.cu_seqlens.data_ptr(), out.kv_lens.data_ptr(),
-         out.slots.data_ptr(), out.positions.data_ptr(), out.mask.data_ptr() if tree else None, ws.data_ptr(), ws.numel())
+         out.slots.data_ptr(), out.positions.data_ptr(), out.mask.data_ptr() if tree else None, ws.data_ptr(), ws.nbytes)
     return out
 
 
@@ -711,8 +717,10 @@ def stem_tree_attn(tree: TreeQ, kv: PagedKV, out=None, lse=None, ws=None, stream
         _need("lse", lse, torch.float32, (hq, T), dev)
     if ws is None:
         ws = _ws(stem_tree_ws_bytes(tree), dev, None)
+    else:
+        _need_ws(ws, dev)
     _run(dev, "stem_tree_attn", LIB.stem_tree_attn, ctypes.byref(desc), ctypes.byref(kv.desc), out.data_ptr(),
-         lse.data_ptr(), ws.data_ptr(), ws.numel())
+         lse.data_ptr(), ws.data_ptr(), ws.nbytes)
     return out, lse, ws
 
 

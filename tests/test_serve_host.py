@@ -260,3 +260,18 @@ def test_oracle_extend_of_a_small_step():
                                         (math.inf, INVALID)])
 def test_tree_plan_refuses_scales_past_fp32(scale, code):
     assert plan(tree(softmax_scale=scale))[0] == code
+
+
+def test_binding_refuses_workspaces_that_are_elsewhere_or_have_gaps():
+    i32 = torch.int32
+    pages = torch.zeros(2, 64, 2, 128, dtype=torch.bfloat16)
+    table = torch.zeros(2, 2, dtype=i32)
+    t = b.make_tree(torch.zeros(4, 4, 128, dtype=torch.bfloat16), torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32), 2)
+    n = b.stem_tree_ws_bytes(t)
+    two = torch.zeros(2, dtype=i32)
+    for ws in (torch.empty(n, dtype=torch.uint8, device="meta"), torch.empty(1, dtype=torch.uint8).expand(n),
+               torch.empty(2 * n, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="ws must be"):
+            b.stem_tree_attn(t, b.paged_kv(pages, pages.clone(), table, 64), ws=ws)
+        with pytest.raises(ValueError, match="ws must be"):
+            b.stem_cache_extend(table, 64, 16, two, two, two, torch.zeros(8, dtype=i32), torch.zeros(1, dtype=i32), 4, ws=ws)
