@@ -218,7 +218,10 @@ cudaError_t launch_cache_extend(const ExtendArgs& args, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(args.seqs) * 4 * sizeof(int32_t);
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(cache_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // the largest step's, once: a smaller one must not lower it under another thread's launch
+    static std::atomic<uint64_t> allowed{0};
+    constexpr size_t kMostSmem = static_cast<size_t>(kMaxExtendSeqs) * 4 * sizeof(int32_t);
+    e = allow_smem(reinterpret_cast<const void*>(cache_extend_kernel), kMostSmem, allowed);
     if (e != cudaSuccess) return e;
   }
   if (ctas > 8) {  // more than the portable cluster

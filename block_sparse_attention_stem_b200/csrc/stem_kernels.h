@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "stem_internal.h"
 
 namespace stem {
@@ -104,6 +106,18 @@ cudaError_t launch_bsa_pair(const BsaMaps& maps, const SeqBatch& batch, const Bs
 cudaError_t launch_vwiden(const void* v8, uint16_t* v16, int total_tokens, int hkv, int hk0, int nhk,
                           const int32_t* cu_seqlens, int num_seqs, const int32_t* page_table, int page_size,
                           int num_pages, int max_pages, cudaStream_t stream);
+
+// Raises a kernel's shared-memory limit, once per device (`done`: a bit for each).
+inline cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+  if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // ---- the paged cache (k_cache_extend.cu, k_rope.cu, k_tree_attn.cu)
 

@@ -3,8 +3,6 @@
 // over a range's items, masks and page lookups.
 #pragma once
 
-#include <atomic>
-
 #include "stem_device.cuh"
 #include "stem_kernels.h"
 
@@ -255,18 +253,6 @@ __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, Rang
     sm.skip = u0 - at;
   }
   return count;
-}
-
-// Raises a kernel's shared-memory limit, once per device (`done`: a bit for each).
-inline cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = -1;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
-  if ((done.load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 // Launches a kernel whose start may overlap the end of the one before it in the

@@ -151,3 +151,35 @@ def test_a_captured_step_advances_its_own_state():
     assert np.array_equal(table.cpu().numpy(), ref_table) and np.array_equal(held.cpu().numpy(), ref_held)
     assert np.array_equal(cache.cpu().numpy(), ref_cache) and int(cursor) == cur
     assert b.stem_read_device_status(out.ws) == 0
+
+
+def test_steps_of_many_sequences_from_two_threads():
+    """Steps of different sizes enqueued at the same time, both past 48 KB of shared memory."""
+    import ctypes
+    import threading
+
+    codes, keep = set(), []
+
+    def work(S, stream):
+        rng = np.random.default_rng(S)
+        cache, new, held, table, pages, free = setup(rng, S, 64, 100, 1, 1, spare=False)
+        ref = C.extend(table, 64, pages, cache, new, held, free, 0, S)
+        with torch.cuda.stream(stream):
+            t, ins = dev(table), [dev(x) for x in (cache, new, held, free, [0])]
+            outs = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (S, 1, S + 1, S, S, S)]
+            ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+        desc = b.StemCacheStep(S, S, 64, pages, t.shape[1], len(free), 0, *[x.data_ptr() for x in ins], None)
+        args = [ctypes.byref(desc), t.data_ptr(), *[x.data_ptr() for x in outs], None, ws.data_ptr(), 256, stream.cuda_stream]
+        keep.append((t, ins, outs, ws, desc, ref))
+        return lambda: codes.update(b.LIB.stem_cache_extend(*args) for _ in range(4000))
+
+    threads = [threading.Thread(target=work(S, torch.cuda.Stream())) for S in (8192, 3500)]
+    torch.cuda.synchronize()
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    assert codes == {b.STEM_OK}
+    for t, _, outs, _, _, ref in keep:
+        assert np.array_equal(t.cpu().numpy(), ref["table"]) and np.array_equal(outs[4].cpu().numpy(), ref["slots"])
