@@ -206,8 +206,10 @@ __global__ void __launch_bounds__(kExtendThreads, 1) cache_extend_kernel(const E
     }
     a.positions[t] = pos;
   }
-  if (bad) set_status(a.status, STEM_ERR_BAD_INPUT_CODE);
-  if (out_of_pages) set_status(a.status, STEM_ERR_OUT_OF_PAGES_CODE);
+  // the larger code stands, whichever thread comes first
+  static_assert(STEM_ERR_OUT_OF_PAGES_CODE > STEM_ERR_BAD_INPUT_CODE, "a step without pages says so");
+  if (out_of_pages) atomicMax(a.status, STEM_ERR_OUT_OF_PAGES_CODE);
+  else if (bad) atomicMax(a.status, STEM_ERR_BAD_INPUT_CODE);
 }
 
 cudaError_t launch_cache_extend(const ExtendArgs& args, cudaStream_t stream) {

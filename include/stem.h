@@ -385,7 +385,8 @@ typedef struct {
  * max_tokens new tokens (those beyond are dropped from every output), a page
  * number outside the pool (slot -1), a parent not below its token (taken as
  * -1) or a token whose mask does not fit mask_words (its bits beyond are
- * dropped).  Nothing outside the arrays is read or written in any case.
+ * dropped).  A step with both reports STEM_ERR_OUT_OF_PAGES.  Nothing outside
+ * the arrays is read or written in any case.
  * One launch; host-side STEM_ERR_INVALID_ARG for sizes and NULL pointers. */
 STEM_API stem_status_t stem_cache_extend(const stem_cache_step_t* step, int32_t* page_table, int32_t* held_out,
                                          int32_t* cursor_out, int32_t* cu_seqlens, int32_t* kv_lens, int32_t* slots,

@@ -183,3 +183,18 @@ def test_steps_of_many_sequences_from_two_threads():
     assert codes == {b.STEM_OK}
     for t, _, outs, _, _, ref in keep:
         assert np.array_equal(t.cpu().numpy(), ref["table"]) and np.array_equal(outs[4].cpu().numpy(), ref["slots"])
+
+
+@pytest.mark.parametrize("cursor", [-1, 45])
+def test_a_step_without_pages_says_so_whatever_else_is_wrong(cursor):
+    """OUT_OF_PAGES is the status of a step that also has values out of range, every time."""
+    rng = np.random.default_rng(8)
+    cache, new, held, table, pages, free = setup(rng, 300, 64, 500, 50, 100, spare=False)
+    T, cache = int(new.sum()), cache.copy()
+    cache[[0, 150, 299]] = -5
+    ref = C.extend(table, 64, pages, cache, new, held, free[:40], cursor, T)
+    assert ref["status"] == {"bad", "pages"}
+    for _ in range(20):
+        _, r, status = run(table, 64, pages, cache, new, held, free[:40], cursor, T)
+        assert status == 9
+    assert np.array_equal(r.slots.cpu().numpy(), ref["slots"])
