@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
   // ---- where this range starts: prefix sum of the sequences' units
   if (threadIdx.x == 0) {
     sm.status = 0;
+    sm.range.bad = 0;
     sm.abort = (smem_u32(smem_raw) & 1023u) != 0;  // the swizzled tiles need this alignment
     if (sm.abort) sm.status = STEM_ERR_TIMEOUT_CODE;
     for (int x = 0; x < 4; ++x) sm.odd_v[x] = 0;
@@ -153,10 +154,10 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
     fence_mbar_init();
   }
   if (warp == kProducer && lane < 3) tma_prefetch_desc(lane == 0 ? &maps.k_pool : lane == 1 ? &maps.q : &maps.v_pool);
-  const int64_t count = find_range<Cfg::kThreads>(a, range, sm.range, &sm.status);
+  const int64_t count = find_range<Cfg::kThreads>(a, range, sm.range);
   if (count == 0) {
     __syncthreads();
-    if (threadIdx.x == 0) a.cta_status[blockIdx.x] = sm.status;
+    if (threadIdx.x == 0) a.cta_status[blockIdx.x] = cta_word(sm.status, sm.range);
     return;
   }
   if (warp == kMmaIssuer) {
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) a.cta_status[blockIdx.x] = sm.status;
+  if (threadIdx.x == 0) a.cta_status[blockIdx.x] = cta_word(sm.status, sm.range);
   if (warp == kMmaIssuer) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -649,17 +650,19 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
 // ---- joining the pieces of the items that were cut (blockIdx.y: item, that is
 // sequence x KV head), in the order of the ranges
 
-// The CTAs' status words become the call's.  One block.
+// The CTAs' status words become the call's, the smaller code if there are two.  One block.
 __device__ __forceinline__ void reduce_status(const TreeArgs& a, int ctas) {
   __shared__ int sm_status;
-  if (threadIdx.x == 0) sm_status = 0;
+  static_assert(STEM_ERR_TIMEOUT_CODE < STEM_ERR_BAD_INPUT_CODE, "a wait that ran out stands");
+  constexpr int kNone = 0x7fffffff;
+  if (threadIdx.x == 0) sm_status = kNone;
   __syncthreads();
   for (int i = threadIdx.x; i < ctas; i += blockDim.x) {
     const int st = a.cta_status[i];
-    if (st != 0) atomicCAS(&sm_status, 0, st);
+    if (st != 0) atomicMin(&sm_status, st);
   }
   __syncthreads();
-  if (threadIdx.x == 0) *a.status = sm_status;
+  if (threadIdx.x == 0) *a.status = sm_status == kNone ? 0 : sm_status;
 }
 
 struct Pieces {

@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8, kRows>::kCtas)
 
   if (threadIdx.x == 0) {
     sm.status = 0;
+    sm.range.bad = 0;
     sm.abort = (smem_u32(smem_raw) & 1023u) != 0;  // the swizzled tiles need this alignment
     if (sm.abort) sm.status = STEM_ERR_TIMEOUT_CODE;
     for (int x = 0; x < 4; ++x) sm.odd_v[x] = 0;
@@ -173,10 +174,10 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8, kRows>::kCtas)
     fence_mbar_init();
   }
   if (warp == kProducer && lane < 3) tma_prefetch_desc(lane == 0 ? &maps.k_pool : lane == 1 ? &maps.q : &maps.v_pool);
-  const int64_t count = find_range<kThreads>(a, blockIdx.x, sm.range, &sm.status);
+  const int64_t count = find_range<kThreads>(a, blockIdx.x, sm.range);
   if (count == 0) {
     __syncthreads();
-    if (threadIdx.x == 0) a.cta_status[blockIdx.x] = sm.status;
+    if (threadIdx.x == 0) a.cta_status[blockIdx.x] = cta_word(sm.status, sm.range);
     return;
   }
   if (warp == kMmaIssuer) {
@@ -666,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, NarrowCfg<kFp8, kRows>::kCtas)
 
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) a.cta_status[blockIdx.x] = sm.status;
+  if (threadIdx.x == 0) a.cta_status[blockIdx.x] = cta_word(sm.status, sm.range);
   if (warp == kMmaIssuer) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);

@@ -197,12 +197,13 @@ struct RangeScratch {
   int64_t scan[16];
   int64_t skip;  // length of first_seq before the range
   int first_seq;
+  int bad;  // bad lengths (the caller clears it first)
 };
-// One __syncthreads inside; the caller's next one publishes skip and first_seq
-// (count is known to every thread).  CTA 0 also writes unit0 for the joining
-// kernel and reports bad lengths.
+// One __syncthreads inside; the caller's next one publishes skip, first_seq and
+// bad (count is known to every thread).  CTA 0 also writes unit0 for the joining
+// kernel and notices bad lengths.
 template <int kThreads>
-__device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, RangeScratch& sm, int* status) {
+__device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, RangeScratch& sm) {
   // the first read of memory that earlier kernels may still be writing
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = warp_id(), lane = lane_id();
@@ -233,7 +234,7 @@ __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, Rang
   const int64_t u0 = range < used ? range_begin(total, used, range) : total;
   const int64_t count = range < used ? range_begin(total, used, range + 1) - u0 : 0;
   if (blockIdx.x == 0) {
-    if (bad) set_status(status, STEM_ERR_BAD_INPUT_CODE);
+    if (bad) sm.bad = 1;
     int64_t at = before;
     for (int s = s_beg; s < s_end; ++s) {
       a.unit0[s] = at;
@@ -253,6 +254,11 @@ __device__ __forceinline__ int64_t find_range(const TreeArgs& a, int range, Rang
     sm.skip = u0 - at;
   }
   return count;
+}
+
+// A CTA's word: a wait that ran out, whose outputs are invalid, stands over bad lengths.
+__device__ __forceinline__ int cta_word(int status, const RangeScratch& sm) {
+  return status != 0 ? status : sm.bad ? STEM_ERR_BAD_INPUT_CODE : 0;
 }
 
 // Launches a kernel whose start may overlap the end of the one before it in the

@@ -505,7 +505,7 @@ STEM_API stem_status_t stem_tree_plan(const stem_tree_t* tree, size_t* ws_bytes)
  * total_tokens (the sequence is skipped), a sequence with more than
  * max_seq_tokens queries (those beyond are skipped), a negative kv_lens (taken
  * as 0) or one past the table's row (the keys beyond are not seen);
- * STEM_ERR_TIMEOUT.  Two launches; the workspace (16-byte aligned) holds nothing
+ * STEM_ERR_TIMEOUT, which stands over the other.  Two launches; the workspace (16-byte aligned) holds nothing
  * between calls, so calls in stream order may share one; calls that may overlap
  * on the GPU need one each. */
 STEM_API stem_status_t stem_tree_attn(const stem_tree_t* tree, const stem_paged_kv_t* kv, void* out, float* lse,
