@@ -61,7 +61,8 @@ void rope_turns(const stem_rope_t& r, RopeArgs* a) {
     long double w = w_j;
     if (r.scaling == STEM_ROPE_LINEAR) w /= r.factor;
     if (r.scaling == STEM_ROPE_YARN) {
-      const double t = std::min(std::max((j - low) / (high - low), 0.0), 1.0);
+      // (a ramp whose ends lie on one side of the pairs: all of them are past it, or none)
+      const double t = high > low ? std::min(std::max((j - low) / (high - low), 0.0), 1.0) : j < low ? 0.0 : 1.0;
       w = w / r.factor * t + w * (1.0 - t);
     }
     a->turn[j] = static_cast<uint64_t>(w * kTurns);  // w <= 1: below 2^62

@@ -406,7 +406,9 @@ typedef enum {
   STEM_ROPE_NTK = 2,     /* w_j from the base base * factor^(r / (r - 2)) */
   STEM_ROPE_YARN = 3     /* w_j (1 - t_j) + w_j / factor t_j with t_j rising from 0 at the pair that makes
                             beta_fast turns over original_len tokens (rounded down) to 1 at the one that
-                            makes beta_slow (rounded up); amplitude 0.1 ln(factor) + 1 */
+                            makes beta_slow (rounded up), kept inside 0 .. r - 1; 1 for every pair when
+                            all make fewer turns than beta_slow, 0 when all make more than beta_fast;
+                            amplitude 0.1 ln(factor) + 1 */
 } stem_rope_scaling_t;
 
 typedef struct {

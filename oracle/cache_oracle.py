@@ -91,7 +91,10 @@ def rope_frequencies(rotary, base=1e6, scaling="plain", factor=1.0, original_len
         low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rotary - 1)
         if low == high:
             high += 0.001
-        t = np.clip((j - low) / (high - low), 0, 1)
+        if high > low:
+            t = np.clip((j - low) / (high - low), 0, 1)
+        else:  # every pair makes fewer turns than beta_slow, or more than beta_fast
+            t = np.full(rotary // 2, 1.0 if pair(beta_slow) <= 0 else 0.0)
         w = w * (1 - t) + w / factor * t
         amp = amplitude or 0.1 * math.log(factor) + 1
     return w, amp

@@ -192,3 +192,17 @@ def test_rows_past_32_bit_offsets():
         rows = p.view(-1, hkv, 128)
         assert torch.equal(rows[slots.long()], x)
         assert int(torch.count_nonzero(rows.view(-1, 1024).any(1))) == 3
+
+
+@pytest.mark.parametrize("freq,same", [
+    (dict(factor=4.0, original_len=4, base=1e4), dict(scaling="linear", factor=4.0, base=1e4)),  # all pairs too slow
+    (dict(factor=8.0, original_len=1), dict(scaling="linear", factor=8.0)),
+    (dict(factor=4.0, original_len=32768, base=10.0), dict(base=10.0))])  # all pairs fast enough
+def test_yarn_whose_ramp_lies_outside_the_pairs(freq, same):
+    """Then every pair is interpolated, or none."""
+    q, k, v = make(40, 4, 2, 11)
+    pos = torch.arange(40, dtype=torch.int32, device="cuda") + 90000
+    one = dict(amplitude=1.0)
+    q1, k1, _ = b.stem_rope(b.make_rope(scaling="yarn", **freq, **one), q, k, v, pos)
+    q2, k2, _ = b.stem_rope(b.make_rope(**same, **one), q, k, v, pos)
+    assert torch.equal(q1, q2) and torch.equal(k1, k2)

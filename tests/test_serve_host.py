@@ -275,3 +275,11 @@ def test_binding_refuses_workspaces_that_are_elsewhere_or_have_gaps():
             b.stem_tree_attn(t, b.paged_kv(pages, pages.clone(), table, 64), ws=ws)
         with pytest.raises(ValueError, match="ws must be"):
             b.stem_cache_extend(table, 64, 16, two, two, two, torch.zeros(8, dtype=i32), torch.zeros(1, dtype=i32), 4, ws=ws)
+
+
+def test_oracle_yarn_outside_the_pairs():
+    w = lambda **kw: C.rope_frequencies(128, **kw)[0]  # noqa: E731
+    assert np.allclose(w(scaling="yarn", factor=4.0, original_len=4, base=1e4), w(base=1e4) / 4, rtol=1e-15)
+    assert np.allclose(w(scaling="yarn", factor=4.0, original_len=32768, base=10.0), w(base=10.0), rtol=1e-15)
+    for n in (1, 4, 7, 40, 256, 32768):  # faster pairs are never interpolated more than slower ones
+        assert np.all(np.diff(w(scaling="yarn", factor=4.0, original_len=n, base=1e4) / w(base=1e4)) <= 1e-15)
