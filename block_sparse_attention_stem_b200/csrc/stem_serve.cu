@@ -41,9 +41,9 @@ void rope_turns(const stem_rope_t& r, RopeArgs* a) {
   constexpr long double kTwoPi = 6.283185307179586476925286766559005768L;
   constexpr long double kTurns = 18446744073709551616.0L / kTwoPi;  // 2^64 to the turn
   const int half = r.rotary_dim / 2;
-  double base = r.base;
+  long double base = r.base;  // (NTK's may pass the range of a double)
   if (r.scaling == STEM_ROPE_NTK)
-    base *= std::pow(r.factor, static_cast<double>(r.rotary_dim) / (r.rotary_dim - 2));
+    base *= std::pow(static_cast<long double>(r.factor), static_cast<long double>(r.rotary_dim) / (r.rotary_dim - 2));
   double low = 0, high = 1;
   if (r.scaling == STEM_ROPE_YARN) {
     // the (fractional) pair that makes `turns` turns over the trained length
@@ -55,7 +55,7 @@ void rope_turns(const stem_rope_t& r, RopeArgs* a) {
     if (low == high) high += 0.001;
   }
   // w_j = ratio^j, carried in 64-bit mantissas: off by at most j 2^-63 of itself
-  const long double ratio = std::pow(static_cast<long double>(base), -2.0L / r.rotary_dim);
+  const long double ratio = std::pow(base, -2.0L / r.rotary_dim);
   long double w_j = 1.0L;
   for (int j = 0; j < half; ++j, w_j *= ratio) {
     long double w = w_j;

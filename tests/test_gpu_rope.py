@@ -206,3 +206,17 @@ def test_yarn_whose_ramp_lies_outside_the_pairs(freq, same):
     q1, k1, _ = b.stem_rope(b.make_rope(scaling="yarn", **freq, **one), q, k, v, pos)
     q2, k2, _ = b.stem_rope(b.make_rope(**same, **one), q, k, v, pos)
     assert torch.equal(q1, q2) and torch.equal(k1, k2)
+
+
+def test_ntk_whose_base_passes_a_double():
+    """The enlarged base is about 10^320: the same angles as with the base that it is (log-space, position 1 to 40)."""
+    q, k, v = make(40, 4, 2, 12)
+    pos = torch.arange(1, 41, dtype=torch.int32, device="cuda")
+    base, factor = 1e300, 1e20
+    qo, _, _ = b.stem_rope(b.make_rope(scaling="ntk", base=base, factor=factor), q, k, v, pos)
+    ln = np.log(base) + 128 / 126 * np.log(factor)
+    ang = f64(pos)[:, None, None] * np.exp(-2.0 * np.arange(64) / 128 * ln)
+    x, y = f64(q)[..., :64], f64(q)[..., 64:]
+    want = np.concatenate([x * np.cos(ang) - y * np.sin(ang), y * np.cos(ang) + x * np.sin(ang)], -1)
+    size = np.tile(np.abs(x) + np.abs(y), 2)
+    assert np.all(np.abs(f64(qo) - want) <= bound(want, size, False))
