@@ -31,9 +31,10 @@
 // by warps of their own.  The largest weight of a row is kept at 2^13 to 2^15.9 of
 // f16's 2^16, since a small weight has to keep its bits where an attention sink
 // takes most of the sum: it is off by 2^-11 of itself down to 2^-27 of the row's
-// largest (19 nats), by 2^-38 of the largest below.  (The reference moves at 2^2.9
-// over it instead of 2^8: sixteen 32-token trees over 16K 172 against 167 us, of
-// 8 tokens 128.0 against 126.4.)
+// largest (19 nats), by 2^-38 of the largest below.  (The reference then moves at
+// 2^2.9 over it instead of 2^8, and with it that of every row of the warp that grew:
+// sixteen 33-63-token trees 197 against 192 us; without the others' 199; at 2^12 and
+// 2^3.9 194.5.)
 //
 // Masked keys: S is replaced by -inf, so nothing in K matters.  A product 0 * v
 // would still carry a NaN or infinity of V into rows that do not see the key,
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(TreeCfg<kFp8>::kThreads, 2)
           const bool need =
               valid && ((m_ref == ninf) ? (m_cand != ninf) : (m_cand > m_ref + Cfg::kSlack));
           if (__any_sync(0xffffffffu, need)) {
-            const float m_new = need ? m_cand : m_ref;
+            const float m_new = valid && m_cand > m_ref ? m_cand : m_ref;  // O is read anyway: every row that grew
             const float alpha = (m_ref == ninf) ? 0.f : fast_exp2(m_ref - m_new);
             l *= alpha;
             if (u > wk.ub) {
