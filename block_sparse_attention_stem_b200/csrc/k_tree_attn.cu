@@ -44,13 +44,15 @@
 //
 // What bounds it.  bf16, one full tile: HBM (eight 32-token trees over 16-32K,
 // 811 MB: the kernel reads 5.67 TB/s, 143 us; 163 us with the join, about 200
-// when the power cap lowers the clock; tensor pipe 57%).  e4m3: instruction
-// issue (51%, four warps per scheduler): exponentials, and widening V, whose bytes
-// HBM would deliver in half the time (sixteen 33-63-token trees, two tiles: 192
-// us).  The roles share one instruction cache: rolling the exponentials and the
-// widening loop took 279 to 222 us, four widening warps at 96 registers 213,
-// fixed addresses without bank conflicts 206 to 192.  Widening by moving bits
-// instead of cvt measured 316 us, keeping the scores in registers with two
+// when the power cap lowers the clock; tensor pipe 57%).  e4m3: no unit is full
+// (sixteen 33-63-token trees, two tiles, 346 MB: 197 to 206 us; issue slots 47%, tensor
+// pipe 32%, HBM 26%), what takes the time is each unit's chain of waits through
+// four roles, with the work done for each of the two tiles: scores read from TMEM
+// twice, V fetched and widened twice.  The roles share one instruction cache.
+// Steps on the way, before the f16 weights were raised: rolling the exponentials
+// and the widening loop took 279 to 222 us, four widening warps at 96 registers
+// 213, fixed addresses without bank conflicts 206 to 192.  Widening by moving
+// bits instead of cvt measured 316 us, keeping the scores in registers with two
 // widening warps 195.
 //
 // 192 threads (320 for e4m3):

@@ -35,10 +35,12 @@
 // instructions that the stream of keys had pushed out of L2 (which the keys'
 // evict-first policy prevents too).
 //
-// Bound by HBM.  Measured: 16 tokens over 16K keys each (1.07 GB) 163 us, 6.59
-// TB/s; 64 over 1 to 8K 169 us; one over 128K (537 MB) 90 us.  Against 32 rows
-// the 128-row kernel is faster (eight tokens of four heads over 16K: 185 against
-// 211 us), since a thread's work grows with the rows.
+// Bound by HBM in bf16.  Measured: 16 tokens over 16K keys each (1.07 GB) 163 us,
+// 6.59 TB/s (reads alone pass what a copy reaches); 64 over 1 to 8K 168 us; one over
+// 128K (537 MB) 90 us.  e4m3: 64 over 1 to 8K (538 MB) 108 us, 5.0 TB/s, a unit's
+// chain of waits.  Against 32 rows the 128-row kernel is faster (eight tokens of
+// four heads over 16K: 185 against 211 us), since a thread's work grows with the
+// rows.
 //
 // 192 threads; bf16: one CTA per SM (216 KB of SMEM, most of it K and V in
 // flight); e4m3: two, because a unit's chain of waits (about 1300 cycles) is as

@@ -187,7 +187,8 @@ constexpr int kNarrowRanges = 148;  // one CTA per SM (e4m3: twice as many, two 
 // Query rows (tokens * group) up to which the narrow kernel is used.  16 rows over
 // 16K keys of 16 sequences: 164 us, against 192 us in the 128-row kernel for 64
 // rows, which costs the same for fewer; for 32 rows a narrow kernel with 32
-// columns took 211 us (e4m3 241), the 128-row kernel 185 (153).
+// columns took 211 us (e4m3 241), the 128-row kernel 185 (153).  16 e4m3 rows over
+// 16K keys of 16 sequences: 109 us, against 126.
 constexpr int kNarrowRows = 16;
 // Units that an item counts beyond its own.  64 tokens over 1 to 8K keys (narrow):
 // none 192 us, one 176, two or three 168; eight 32-token trees over 16-32K: none

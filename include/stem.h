@@ -335,7 +335,9 @@ STEM_API stem_status_t stem_noalloc_read_device_status(stem_stream_t stream, ste
  * The pages have no counterpart (they end at the prefill layer); the page
  * layout is stem_paged_kv_t's, so stem_bsa_fwd_paged reads the same pages.
  * Lengths live on the device, so a captured step can be replayed while they
- * grow.
+ * grow.  stem_bsa_fwd_paged also reads the rows from a sequence's end to its next
+ * block; nothing here writes those, so a pool that it reads has to start out
+ * finite (zeros).
  * ------------------------------------------------------------------------ */
 
 /* One step of num_seqs sequences: sequence s has cache_lens[s] tokens in the
@@ -498,7 +500,10 @@ STEM_API stem_status_t stem_tree_plan(const stem_tree_t* tree, size_t* ws_bytes)
  *   kv_lens[s] < n - j is not there to see).
  *   out[t][h] = sum softmax(sigma q_t . k_u) v_u,  lse[h][t] = ln sum exp(sigma q_t . k_u)
  * out bf16 [T, Hq, d]; lse fp32 [Hq][T].  A query that sees no key gives out = 0
- * and lse = -inf.  Rows of out and lse that belong to no sequence are left as
+ * and lse = -inf.  Logits, sums and O are fp32.  A weight of the sum over v keeps
+ * 15 bits in bf16; in e4m3 it is off by at most 2^-10 of itself down to 2^-27 of the
+ * row's largest (19 nats), below that by at most 2^-38 of the largest: 2^-38 max |v| per
+ * key, under the rounding of the fp32 sums.  Rows of out and lse that belong to no sequence are left as
  * they were.  K and V of keys that a query does not see may hold anything,
  * infinities and NaN included, and so may rows of pages behind kv_lens[s].  A
  * page number outside the pool reads zeros.  The work is split over the keys by
